@@ -189,7 +189,8 @@ def plain_norm(st):
 
 def to8(x):
     """Rows of fp32 values as 8-bit integers (held in fp32) and their scales."""
-    s = x.abs().amax(dim=1, keepdim=True) / 127.0
+    big = x.abs().amax(dim=1, keepdim=True)
+    s = big / torch.full_like(big, 127.0)  # by a tensor: a true division (by a number torch multiplies by 1 / 127)
     return torch.where(s > 0, (x / s).round().clamp(-127, 127), torch.zeros_like(x)), s
 
 
