@@ -18,7 +18,9 @@ Calls (same names as the C ABI):
 plus ``workspace(desc, m, x_dtype, device)`` and ``gemm_workspace(...)``, zero-filled
 device buffers for gemv_ws / gemm_ws, and ``VQLinear``, a layer object holding the packed
 weights that picks gemv_ws or gemm_ws by batch size, the analogue of the VPTQ guide's
-``VPTQLinear`` module.
+``VPTQLinear`` module.  The 8-bit operators (layers kept in 8 bits, their experts, the norms
+between blocks) are in ``q8`` and re-exported here: q8_*, expert_*, block_norm, Q8Linear,
+Q8Experts.
 """
 from __future__ import annotations
 
@@ -48,7 +50,9 @@ EXPORTED = ("vq_abi_version", "vq_status_string", "vq_packed_bytes", "vq_pack", 
             "vq_gemv_workspace_bytes", "vq_gemv_ws", "vq_gemm", "vq_svq_dequant", "vq_svq_gemv", "vq_rht", "vq_rht_block",
             "vq_assign_workspace_bytes", "vq_assign", "vq_svq_gemm", "vq_gemv_noalloc", "vq_svq_pack",
             "vq_gemm_workspace_bytes", "vq_gemm_ws", "vq_rht_product_workspace_bytes", "vq_gemv_ws_rht",
-            "vq_gemm_ws_rht")
+            "vq_gemm_ws_rht", "vq_q8_row_bytes", "vq_q8_quantize", "vq_q8_gemm_workspace_bytes", "vq_q8_gemm",
+            "vq_q8_linear_workspace_bytes", "vq_q8_linear", "vq_expert_plan", "vq_q8_gemm_grouped", "vq_expert_combine",
+            "vq_q8_experts_workspace_bytes", "vq_q8_experts", "vq_block_norm")
 
 
 class Desc(ctypes.Structure):
@@ -121,6 +125,7 @@ def _load():
     lib.vq_assign_workspace_bytes.restype = ctypes.c_int
     lib.vq_assign.argtypes = [dp, vp, ctypes.c_int, vp, vp, vp, vp, vp, sz, vp]
     lib.vq_assign.restype = ctypes.c_int
+    q8.bind(lib)
     return lib
 
 
@@ -531,3 +536,9 @@ class VQLinear:
         return y.reshape(*lead, self.desc.out_features)
 
     __call__ = forward
+
+
+from . import q8  # noqa: E402  (uses the helpers above)
+from .q8 import (NORM_LAYER, NORM_NONE, NORM_RMS, NormDesc, Q8Experts, Q8Linear, block_norm, expert_combine,  # noqa: E402,F401
+                 expert_plan, q8_experts, q8_experts_workspace_bytes, q8_gemm, q8_gemm_grouped,
+                 q8_gemm_workspace_bytes, q8_linear, q8_linear_workspace_bytes, q8_pad, q8_quantize, q8_row_bytes)

@@ -140,4 +140,71 @@ size_t assign_workspace(const vq_desc& d);
 vq_status launch_assign(const vq_desc& d, const void* w, vq_dtype w_dtype, const uint16_t* cb1, const uint16_t* cb2,
                         uint32_t* idx1, uint32_t* idx2, void* workspace, void* stream);
 
+// ---- 8-bit operators (vq_q8_*, vq_expert_*, vq_block_norm) ----
+
+// Whether a launch of `blocks` workgroups of `threads` stays inside the 32-bit grid.
+inline bool grid_ok(int64_t blocks, int64_t threads) { return blocks >= 1 && blocks * threads <= 0xFFFFFFFFll; }
+
+// Bytes of one row of an 8-bit matrix of k columns: whole 128-byte matrix steps, the pad zero.
+constexpr int64_t q8_row_bytes(int64_t k) { return (k + 127) / 128 * 128; }
+// Largest K of the products and longest row of the row pass, which holds a row in the registers of one workgroup.  (An
+// int32 sum would hold 131071 products of magnitude 128 * 128.)
+constexpr int32_t kQ8MaxK = 65536;
+constexpr int32_t kNormMaxDim = 65536;
+
+// The row pass between two layers (validated arguments; vq_norm.hip).
+struct NormArgs {
+  int32_t rows, dim;
+  const void* z;
+  vq_dtype z_dtype;
+  int64_t ldz;  // elements
+  const void* h;  // residual or nullptr
+  vq_dtype h_dtype;  // also r's
+  int64_t ldh;
+  int32_t post, pre;  // vq_norm_kind
+  const void *post_w, *post_b, *pre_w, *pre_b;  // [dim] or nullptr
+  vq_dtype w_dtype;
+  const void* gate;  // [ceil(rows / gate_rows)][dim] or nullptr
+  vq_dtype gate_dtype;
+  int32_t gate_rows;
+  float eps, w_offset, res_scale, gate_scale;
+  int32_t combine;  // a residual or a gate_scale other than 1
+  void* r;          // [rows][dim] or nullptr
+  void* x;          // [rows][dim] or nullptr
+  vq_dtype x_dtype;
+  uint8_t* q;  // [rows][q8_row_bytes(dim)] or nullptr
+  float* s;    // [rows]
+};
+vq_status launch_norm(const NormArgs& a, void* stream);
+
+// An 8-bit product, dense (experts == 0) or grouped by expert (validated arguments; vq_q8.hip).
+struct Q8Args {
+  int32_t m;         // dense: rows; grouped: bound of the sorted rows, offsets[experts] at most
+  int32_t tokens;    // rows of q and s
+  int32_t n;         // outputs (with the gate: w has 2 n rows)
+  int32_t k;
+  const uint8_t* q;  // [tokens][q8_row_bytes(k)]
+  const float* s;    // [tokens]
+  const uint8_t* w;  // dense [n][..], grouped [experts][n or 2 n][..]
+  const float* sw;
+  const uint16_t* bias;  // fp16 [n] / [experts][n or 2 n] or nullptr
+  void* y;               // [m][n]
+  vq_dtype y_dtype;
+  int32_t experts;
+  const int32_t* offsets;  // [experts + 1]
+  const int32_t* rows;     // [m] token of each sorted row, or nullptr: the row itself
+  int32_t gated;           // y = silu(g) u, g and u the two halves of w's rows
+  int32_t* part;           // [splits][m][n] int32 partial sums (splits > 1)
+  int32_t splits;
+};
+// K splits that a dense product of this shape uses; its workspace is splits * m * n int32 where splits > 1.
+int32_t q8_splits(int32_t m, int32_t n, int32_t k);
+vq_status launch_q8(const Q8Args& a, void* stream);
+
+// Routing (vq_experts.hip): ids [tokens * top] -> offsets [experts + 1], rows and pos [tokens * top].
+vq_status launch_expert_plan(int32_t tokens, int32_t top, int32_t experts, const int32_t* ids, int32_t* offsets,
+                             int32_t* rows, int32_t* pos, void* stream);
+vq_status launch_expert_combine(int32_t tokens, int32_t top, int32_t n, int32_t rows, const float* z,
+                                const int32_t* pos, const float* p, void* y, vq_dtype y_dtype, void* stream);
+
 }  // namespace vqi

@@ -380,6 +380,117 @@ vq_status vq_assign_workspace_bytes(const vq_desc* desc, size_t* nbytes);
 vq_status vq_assign(const vq_desc* desc, const void* w, vq_dtype w_dtype, const void* cb1, const void* cb2,
                     uint32_t* idx1, uint32_t* idx2, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * 8-bit operators: what a block with some layers kept in 8 bits runs next to its codebook
+ * layers.  Everything above on ownership, streams and errors holds for them: device
+ * pointers, the caller's stream and workspace, arguments checked before any launch.
+ *
+ * An 8-bit matrix of k columns is stored in rows of vq_q8_row_bytes(k) = 128 ceil(k / 128)
+ * bytes, one int8 per column, the pad bytes ZERO (vq_q8_quantize and vq_block_norm write
+ * them so; a caller that lays out weights itself has to), with one fp32 scale per row:
+ * value = q * s.  1 <= k <= 65536, so that every sum of products fits an int32; the sums
+ * are exact.  Rows are written with
+ *     s = fp32(max|x| / 127),  q = fp32(x / s) rounded to the nearest integer, ties to even,
+ * within +-127.  A zero row has s = 0 and q = 0.  A row that holds an infinity or a NaN has
+ * s = NaN and q = 0: the token's whole output is then NaN, and no other token's.
+ */
+
+/* Bytes of one row of an 8-bit matrix of k columns (0 for k < 1). */
+int64_t vq_q8_row_bytes(int32_t k);
+
+/* x [rows][k] (row stride ldx >= k elements; x_dtype fp16, bf16 or fp32, element-aligned) ->
+ * q [rows][vq_q8_row_bytes(k)] int8 (16-byte aligned), s [rows] fp32. */
+vq_status vq_q8_quantize(int32_t rows, int32_t k, const void* x, vq_dtype x_dtype, int64_t ldx, void* q, float* s,
+                         void* stream);
+
+/* y [M][N] = (sum_k q[m][k] w[n][k]) * s[m] * sw[n] (+ bias[n]): q [M] and w [N] rows of K
+ * columns (16-byte aligned), s [M] and sw [N] fp32, bias fp16 [N] or NULL, y_dtype fp16,
+ * bf16 or fp32.  Any M >= 0.  `workspace` (256-byte aligned) holds the int32 partial sums of
+ * products that cut K over the CUs; NULL (or a shape that needs none: 0 bytes) computes the
+ * same y, bit for bit, without cutting it. */
+vq_status vq_q8_gemm_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t* nbytes);
+vq_status vq_q8_gemm(int32_t M, int32_t N, int32_t K, const void* q, const float* s, const void* w, const float* sw,
+                     const void* bias, void* y, vq_dtype y_dtype, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* vq_q8_gemm on x [M][K] (row stride ldx elements, fp16, bf16 or fp32) cut to 8 bits inside the call: the same y as
+ * vq_q8_quantize followed by vq_q8_gemm.  The workspace is required where vq_q8_linear_workspace_bytes
+ * is not 0. */
+vq_status vq_q8_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t* nbytes);
+vq_status vq_q8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype x_dtype, int64_t ldx, const void* w,
+                       const float* sw, const void* bias, void* y, vq_dtype y_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Routing plan of `tokens` tokens with `top` expert ids each, ids int32 [tokens][top]:
+ *   offsets [experts + 1]   sorted rows offsets[e] .. offsets[e + 1] - 1 belong to expert e
+ *   rows    [tokens * top]  token of each sorted row, in ascending order of (token, slot)
+ *                           within an expert; entries from offsets[experts] on are not written
+ *   pos     [tokens * top]  sorted row of each (token, slot), -1 where the id is not in
+ *                           [0, experts): such a pair is dropped (a padded token, an expert
+ *                           of another rank)
+ * 1 <= experts <= 4096, top >= 1, tokens * top < 2^30. */
+vq_status vq_expert_plan(int32_t tokens, int32_t top, int32_t experts, const int32_t* ids, int32_t* offsets,
+                         int32_t* rows, int32_t* pos, void* stream);
+
+/* The 8-bit product grouped by expert, the group sizes on the device.  Sorted row r of expert e
+ * (offsets as written by vq_expert_plan, offsets[experts] <= max_rows) is token rows[r] of
+ * q [tokens], s [tokens] (rows NULL: token r, then tokens >= max_rows):
+ *   gated == 0: y[r][n] = (sum_k q w[e][n]) * s * sw[e][n] (+ bias[e][n]),      w [experts][N]
+ *   gated == 1: y[r][n] = silu(g) * u, g and u such products with rows n and N + n of
+ *               w [experts][2 N], sw [experts][2 N], bias [experts][2 N]
+ * y [max_rows][N]; rows from offsets[experts] on are not written. */
+vq_status vq_q8_gemm_grouped(int32_t experts, int32_t max_rows, int32_t tokens, int32_t N, int32_t K,
+                             const int32_t* offsets, const int32_t* rows, const void* q, const float* s, const void* w,
+                             const float* sw, const void* bias, int32_t gated, void* y, vq_dtype y_dtype, void* stream);
+
+/* y [tokens][N] = sum over a token's slots j, in order, of p[t][j] * z[pos[t][j]], in fp32:
+ * z fp32 [max_rows][N], pos from vq_expert_plan (slots with pos outside [0, max_rows) add
+ * nothing), p fp32 [tokens][top]. */
+vq_status vq_expert_combine(int32_t tokens, int32_t top, int32_t N, int32_t max_rows, const float* z,
+                            const int32_t* pos, const float* p, void* y, vq_dtype y_dtype, void* stream);
+
+/* A whole expert layer: for x [tokens][D] (row stride ldx), ids int32 and p fp32 [tokens][top],
+ *   y[t] = sum_j p[t][j] * (W_out[e] h),  h = silu(g) * u in 8 bits per row,
+ *   (g, u) = W_in[e] x[t] with x[t] in 8 bits,  e = ids[t][j]
+ * w_in [experts][2 I] rows of D columns (gate rows first), w_out [experts][D] rows of I columns,
+ * s_in [experts][2 I], s_out [experts][D] fp32; y [tokens][D].  Ids outside [0, experts) add
+ * nothing. */
+vq_status vq_q8_experts_workspace_bytes(int32_t tokens, int32_t top, int32_t experts, int32_t D, int32_t I,
+                                        size_t* nbytes);
+vq_status vq_q8_experts(int32_t tokens, int32_t top, int32_t experts, int32_t D, int32_t I, const void* x,
+                        vq_dtype x_dtype, int64_t ldx, const int32_t* ids, const float* p, const void* w_in,
+                        const float* s_in, const void* w_out, const float* s_out, void* y, vq_dtype y_dtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum vq_norm_kind { VQ_NORM_NONE = 0, VQ_NORM_RMS = 1, VQ_NORM_LAYER = 2 } vq_norm_kind;
+
+/* Shapes, types and constants of vq_block_norm. */
+typedef struct vq_norm_desc {
+  int32_t rows, dim;   /* 1 <= dim <= 65536 */
+  int32_t post, pre;   /* vq_norm_kind of N_post and N_pre */
+  vq_dtype z_dtype;    /* z: fp16, bf16 or fp32, as every type here */
+  vq_dtype h_dtype;    /* h and r */
+  vq_dtype w_dtype;    /* norm weights and biases */
+  vq_dtype gate_dtype;
+  vq_dtype x_dtype;
+  int32_t gate_rows;   /* rows that share one gate row: gate [ceil(rows / gate_rows)][dim]; >= 1 */
+  float eps, w_offset; /* N multiplies by w_offset + w (w_offset 1: weights stored about zero) */
+  float res_scale, gate_scale;
+  int64_t ldz, ldh;    /* row strides of z and h in elements, >= dim */
+} vq_norm_desc;
+
+/* Between two blocks, one pass over the rows, everything in fp32 and rounded once at the store:
+ *   r = res_scale * h + gate_scale * gate * N_post(z),   x = N_pre(r)
+ *   N(a) = (a - mean) / sqrt(mean((a - mean)^2) + eps) * (w_offset + w) + b
+ * mean is 0 for VQ_NORM_RMS; VQ_NORM_NONE is the identity and takes no weights.  h, gate, the
+ * weights and the biases [dim] may each be NULL (no residual, 1, no factor, 0).  Outputs, each
+ * NULL if not wanted, at least one given: r [rows][dim] in h_dtype (it may be h itself where
+ * ldh == dim), x [rows][dim] in x_dtype, and q, s (both or neither): x in 8 bits, from its
+ * fp32 values.  Pointers are element-aligned, q 16-byte aligned. */
+vq_status vq_block_norm(const vq_norm_desc* desc, const void* z, const void* h, const void* post_w, const void* post_b,
+                        const void* pre_w, const void* pre_b, const void* gate, void* r, void* x, void* q, float* s,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif
