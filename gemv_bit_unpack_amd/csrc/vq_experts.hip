@@ -1,6 +1,7 @@
 // Routing for the products grouped by expert: vq_expert_plan sorts the chosen (token, slot) pairs by expert,
 // vq_expert_combine joins a token's expert rows with its router weights.
 #include "vq_device.h"
+#include "vq_q8_device.h"
 
 namespace {
 
@@ -93,8 +94,7 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(int32_t tokens, int
       __builtin_memcpy((float*)y + at, acc, 16);
     } else {
       uint16_t h[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = y_dtype == VQ_F16 ? vqd::f32_to_f16_rne(acc[k]) : vqd::f32_to_bf16_rne(acc[k]);
+      vqd::narrow<4>(acc, y_dtype, h);
       __builtin_memcpy((uint16_t*)y + at, h, 8);
     }
   } else {

@@ -80,8 +80,7 @@ __device__ __forceinline__ void store_run(void* y, vq_dtype t, int64_t row_at, i
       __builtin_memcpy((float*)y + row_at + n, v, 4 * CNT);
     } else {
       uint16_t h[CNT];
-#pragma unroll
-      for (int k = 0; k < CNT; ++k) h[k] = t == VQ_F16 ? vqd::f32_to_f16_rne(v[k]) : vqd::f32_to_bf16_rne(v[k]);
+      vqd::narrow<CNT>(v, t, h);
       __builtin_memcpy((uint16_t*)y + row_at + n, h, 2 * CNT);
     }
   } else {

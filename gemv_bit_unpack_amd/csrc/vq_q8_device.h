@@ -5,7 +5,27 @@
 
 #include <cstdint>
 
+#include "vq_device.h"
+
 namespace vqd {
+
+// fp32 -> 16-bit type `t`, rounded to nearest even by the hardware conversions (bf16: two values per instruction).
+template <int CNT>
+__device__ __forceinline__ void narrow(const float (&f)[CNT], vq_dtype t, uint16_t (&v)[CNT]) {
+  if (t == VQ_F16) {
+#pragma unroll
+    for (int k = 0; k < CNT; ++k) v[k] = f32_to_f16_rne(f[k]);
+  } else {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int k = 0; k < CNT; k += 2) {
+      const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{f[k], f[k + 1]}), b2));
+      v[k] = (uint16_t)w;
+      v[k + 1] = (uint16_t)(w >> 16);
+    }
+  }
+}
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu; }
 

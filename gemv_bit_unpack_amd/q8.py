@@ -16,6 +16,7 @@ plus the layer objects ``Q8Linear`` and ``Q8Experts``, which keep a workspace pe
 from __future__ import annotations
 
 import ctypes
+import functools
 
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 _KINDS = {"none": NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
@@ -54,53 +55,79 @@ def bind(lib):
     lib.vq_q8_row_bytes.restype = i64
 
 
-from . import VQ_F32, _check, _dev_ptr, _dtype_code, _stream_ptr, _torch, lib  # noqa: E402
+from . import VQ_BF16, VQ_F16, VQ_F32, _check, _torch, lib  # noqa: E402
+
+_codes = {}
 
 
-def _float_dtypes():
-    torch = _torch()
-    return (torch.float16, torch.bfloat16, torch.float32)
+def _code(dt):
+    """vq_dtype of a torch dtype."""
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.float16: VQ_F16, torch.bfloat16: VQ_BF16, torch.float32: VQ_F32})
+    code = _codes.get(dt)
+    if code is None:
+        raise TypeError("unsupported dtype %s, expected fp16, bf16 or fp32" % dt)
+    return code
 
 
-def _rows_ptr(t, what):
-    """Pointer and row stride of a 2-d device tensor whose rows are contiguous."""
+def _stream(dev):
+    """Handle of the current stream of device index dev."""
+    return _torch().cuda.current_stream(dev).cuda_stream
+
+
+def _device(t, what):
+    """Device index of a device tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a device tensor" % what)
+    return dev
+
+
+def _rows(t, what):
+    """(pointer, row stride, dtype code, device index) of a 2-d device tensor whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError("%s must be 2-d, got %s" % (what, tuple(t.shape)))
-    if not t.is_cuda:
-        raise ValueError("%s must be a device tensor" % what)
-    if t.dtype not in _float_dtypes():
-        raise TypeError("%s has dtype %s, expected fp16, bf16 or fp32" % (what, t.dtype))
+    dev = _device(t, what)
     m, k = t.shape
-    if k > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), k, _code(t.dtype), dev
+    ld, one = t.stride()
+    if k > 1 and one != 1:
         raise ValueError("%s must have contiguous rows" % what)
-    ld = t.stride(0) if m > 1 else k
+    if m <= 1:
+        ld = k
     if ld < k:
         raise ValueError("%s must not have overlapping rows" % what)
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.data_ptr(), ld, _code(t.dtype), dev
 
 
-def _expect(t, what, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _ptr(t, what, shape, dev, dtype=None):
+    """Pointer of a contiguous tensor of the given shape (None: any) on device dev (None for no tensor)."""
+    if t is None:
+        return None
+    if shape is not None and tuple(t.shape) != shape:
         raise ValueError("%s must be %s, got %s" % (what, list(shape), tuple(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on device %d, is on %s" % (what, dev, t.device))
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (what, t.dtype, dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t.data_ptr()
 
 
-def _same_device(ref, **others):
-    for what, t in others.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError("%s is on %s, expected %s" % (what, t.device, ref.device))
+def _ws(ws, dev):
+    """(pointer, bytes) of a workspace."""
+    return (None, 0) if ws is None else (_ptr(ws, "workspace", None, dev), ws.numel() * ws.element_size())
 
 
-def _ws_args(ws):
-    return (None, 0) if ws is None else (_dev_ptr(ws, "workspace"), ws.numel() * ws.element_size())
+def _out(out, shape, dtype, like):
+    """An output of this shape: `out` itself, checked by _ptr later, or a new tensor on like's device."""
+    return like.new_empty(shape, dtype=dtype) if out is None else out
 
 
-def _out(out, shape, dtype, device):
-    if out is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    _expect(out, "out", shape)
-    return out
-
-
+@functools.lru_cache(maxsize=4096)
 def q8_row_bytes(k: int) -> int:
     """Bytes of one row of an 8-bit matrix of k columns."""
     return int(lib().vq_q8_row_bytes(int(k)))
@@ -119,20 +146,20 @@ def q8_quantize(x, out=None):
     """Rows of x [M, K] (fp16, bf16 or fp32; any row stride) in 8 bits: (q int8 [M, q8_row_bytes(K)], s fp32 [M]).
     ``out``: the pair to write into."""
     torch = _torch()
-    p, ld = _rows_ptr(x, "x")
+    p, ld, code, dev = _rows(x, "x")
     m, k = x.shape
+    row = q8_row_bytes(k)
     q, s = out or (None, None)
-    q = _out(q, (m, q8_row_bytes(k)), torch.int8, x.device)
-    s = _out(s, (m,), torch.float32, x.device)
-    _same_device(x, q=q, s=s)
-    _check(lib().vq_q8_quantize(m, k, p, _dtype_code(x.dtype), ld, _dev_ptr(q, "q", (torch.int8,)),
-                                _dev_ptr(s, "s", (torch.float32,)), _stream_ptr(x.device)), "vq_q8_quantize")
+    q, s = _out(q, (m, row), torch.int8, x), _out(s, (m,), torch.float32, x)
+    _check(lib().vq_q8_quantize(m, k, p, code, ld, _ptr(q, "q", (m, row), dev, torch.int8),
+                                _ptr(s, "s", (m,), dev, torch.float32), _stream(dev)), "vq_q8_quantize")
     return q, s
 
 
+@functools.lru_cache(maxsize=4096)
 def _bytes_of(fn, *shape):
     n = ctypes.c_size_t(0)
-    _check(getattr(lib(), fn)(*(int(v) for v in shape), ctypes.byref(n)), fn)
+    _check(getattr(lib(), fn)(*shape, ctypes.byref(n)), fn)
     return int(n.value)
 
 
@@ -154,30 +181,26 @@ def q8_gemm(q, s, w, sw, bias, k, ws=None, y_dtype=None, out=None):
     ``ws``: a uint8 device buffer of q8_gemm_workspace_bytes(M, N, k) (None: the product does not cut K).  Calls that
     share a workspace must be ordered (one stream)."""
     torch = _torch()
-    m, n = q.shape[0], w.shape[0]
-    ld = q8_row_bytes(k)
-    _expect(q, "q", (m, ld)), _expect(w, "w", (n, ld)), _expect(s, "s", (m,)), _expect(sw, "sw", (n,))
-    _expect(bias, "bias", (n,))
-    out = _out(out, (m, n), y_dtype or torch.bfloat16, q.device)
-    _same_device(q, s=s, w=w, sw=sw, bias=bias, ws=ws, out=out)
-    i8, f32 = (torch.int8,), (torch.float32,)
-    _check(lib().vq_q8_gemm(m, n, k, _dev_ptr(q, "q", i8), _dev_ptr(s, "s", f32), _dev_ptr(w, "w", i8),
-                            _dev_ptr(sw, "sw", f32), _dev_ptr(bias, "bias", (torch.float16,)), _dev_ptr(out, "out"),
-                            _dtype_code(out.dtype), *_ws_args(ws), _stream_ptr(q.device)), "vq_q8_gemm")
+    dev = _device(q, "q")
+    m, n, row = q.shape[0], w.shape[0], q8_row_bytes(k)
+    out = _out(out, (m, n), y_dtype or torch.bfloat16, q)
+    f32 = torch.float32
+    _check(lib().vq_q8_gemm(m, n, k, _ptr(q, "q", (m, row), dev, torch.int8), _ptr(s, "s", (m,), dev, f32),
+                            _ptr(w, "w", (n, row), dev, torch.int8), _ptr(sw, "sw", (n,), dev, f32),
+                            _ptr(bias, "bias", (n,), dev, torch.float16), _ptr(out, "out", (m, n), dev),
+                            _code(out.dtype), *_ws(ws, dev), _stream(dev)), "vq_q8_gemm")
     return out
 
 
 def q8_linear(x, w, sw, bias, ws, y_dtype=None, out=None):
     """q8_gemm on x [M, K] cut to 8 bits inside the call; ``ws``: a uint8 device buffer of q8_linear_workspace_bytes."""
     torch = _torch()
-    p, ld = _rows_ptr(x, "x")
+    p, ld, code, dev = _rows(x, "x")
     (m, k), n = x.shape, w.shape[0]
-    _expect(w, "w", (n, q8_row_bytes(k))), _expect(sw, "sw", (n,)), _expect(bias, "bias", (n,))
-    out = _out(out, (m, n), y_dtype or x.dtype, x.device)
-    _same_device(x, w=w, sw=sw, bias=bias, ws=ws, out=out)
-    _check(lib().vq_q8_linear(m, n, k, p, _dtype_code(x.dtype), ld, _dev_ptr(w, "w", (torch.int8,)),
-                              _dev_ptr(sw, "sw", (torch.float32,)), _dev_ptr(bias, "bias", (torch.float16,)),
-                              _dev_ptr(out, "out"), _dtype_code(out.dtype), *_ws_args(ws), _stream_ptr(x.device)),
+    out = _out(out, (m, n), y_dtype or x.dtype, x)
+    _check(lib().vq_q8_linear(m, n, k, p, code, ld, _ptr(w, "w", (n, q8_row_bytes(k)), dev, torch.int8),
+                              _ptr(sw, "sw", (n,), dev, torch.float32), _ptr(bias, "bias", (n,), dev, torch.float16),
+                              _ptr(out, "out", (m, n), dev), _code(out.dtype), *_ws(ws, dev), _stream(dev)),
            "vq_q8_linear")
     return out
 
@@ -187,11 +210,13 @@ def expert_plan(ids, experts: int):
     torch = _torch()
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, top], got %s" % (tuple(ids.shape),))
+    dev = _device(ids, "ids")
     t, top = ids.shape
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)
-    offsets, rows, pos = new(int(experts) + 1), new(t * top), new(t, top)
-    _check(lib().vq_expert_plan(t, top, int(experts), _dev_ptr(ids, "ids", (torch.int32,)), _dev_ptr(offsets, "offsets"),
-                                _dev_ptr(rows, "rows"), _dev_ptr(pos, "pos"), _stream_ptr(ids.device)), "vq_expert_plan")
+    # refused sizes are the library's to name; it is given no buffer for them
+    offsets = ids.new_empty((max(int(experts), 0) + 1,), dtype=torch.int32)
+    rows, pos = ids.new_empty((t * top,), dtype=torch.int32), ids.new_empty((t, top), dtype=torch.int32)
+    _check(lib().vq_expert_plan(t, top, int(experts), _ptr(ids, "ids", (t, top), dev, torch.int32), offsets.data_ptr(),
+                                rows.data_ptr(), pos.data_ptr(), _stream(dev)), "vq_expert_plan")
     return offsets, rows, pos
 
 
@@ -199,37 +224,34 @@ def q8_gemm_grouped(offsets, rows, q, s, w, sw, bias, k, max_rows, gated=False, 
     """The 8-bit product grouped by expert (vq_q8_gemm_grouped): y [max_rows, N] over sorted rows, w [E, N or 2 N, ..];
     ``rows`` None: sorted row r is row r of q.  Rows from offsets[E] on are not written."""
     torch = _torch()
+    dev = _device(q, "q")
     e, nw = w.shape[0], w.shape[1]
     if gated and nw % 2:
         raise ValueError("a gated w must have an even number of rows, got %d" % nw)
-    n, ld = nw // 2 if gated else nw, q8_row_bytes(k)
-    t = q.shape[0]
-    _expect(q, "q", (t, ld)), _expect(s, "s", (t,)), _expect(w, "w", (e, nw, ld)), _expect(sw, "sw", (e, nw))
-    _expect(bias, "bias", (e, nw)), _expect(offsets, "offsets", (e + 1,))
+    n, row, t = nw // 2 if gated else nw, q8_row_bytes(k), q.shape[0]
     if rows is not None and rows.numel() < max_rows:
         raise ValueError("rows must have at least max_rows = %d entries, got %d" % (max_rows, rows.numel()))
-    out = _out(out, (max_rows, n), y_dtype or torch.float32, q.device)
-    _same_device(q, offsets=offsets, rows=rows, s=s, w=w, sw=sw, bias=bias, out=out)
-    i8, i32, f32 = (torch.int8,), (torch.int32,), (torch.float32,)
-    _check(lib().vq_q8_gemm_grouped(e, max_rows, t, n, k, _dev_ptr(offsets, "offsets", i32), _dev_ptr(rows, "rows", i32),
-                                    _dev_ptr(q, "q", i8), _dev_ptr(s, "s", f32), _dev_ptr(w, "w", i8),
-                                    _dev_ptr(sw, "sw", f32), _dev_ptr(bias, "bias", (torch.float16,)),
-                                    int(bool(gated)), _dev_ptr(out, "out"), _dtype_code(out.dtype),
-                                    _stream_ptr(q.device)), "vq_q8_gemm_grouped")
+    out = _out(out, (max_rows, n), y_dtype or torch.float32, q)
+    i8, i32, f32 = torch.int8, torch.int32, torch.float32
+    _check(lib().vq_q8_gemm_grouped(e, max_rows, t, n, k, _ptr(offsets, "offsets", (e + 1,), dev, i32),
+                                    _ptr(rows, "rows", None, dev, i32), _ptr(q, "q", (t, row), dev, i8),
+                                    _ptr(s, "s", (t,), dev, f32), _ptr(w, "w", (e, nw, row), dev, i8),
+                                    _ptr(sw, "sw", (e, nw), dev, f32), _ptr(bias, "bias", (e, nw), dev, torch.float16),
+                                    int(bool(gated)), _ptr(out, "out", (max_rows, n), dev), _code(out.dtype),
+                                    _stream(dev)), "vq_q8_gemm_grouped")
     return out
 
 
 def expert_combine(z, pos, p, y_dtype=None, out=None):
     """y [T, N] = sum_j p[t, j] z[pos[t, j]] of z fp32 [R, N], pos int32 and p fp32 [T, top]."""
     torch = _torch()
-    t, top = pos.shape
-    r, n = z.shape
-    _expect(p, "p", (t, top))
-    out = _out(out, (t, n), y_dtype or torch.float32, pos.device)
-    _same_device(pos, z=z, p=p, out=out)
-    _check(lib().vq_expert_combine(t, top, n, r, _dev_ptr(z, "z", (torch.float32,)), _dev_ptr(pos, "pos", (torch.int32,)),
-                                   _dev_ptr(p, "p", (torch.float32,)), _dev_ptr(out, "out"), _dtype_code(out.dtype),
-                                   _stream_ptr(pos.device)), "vq_expert_combine")
+    dev = _device(pos, "pos")
+    (t, top), (r, n) = pos.shape, z.shape
+    out = _out(out, (t, n), y_dtype or torch.float32, pos)
+    _check(lib().vq_expert_combine(t, top, n, r, _ptr(z, "z", (r, n), dev, torch.float32),
+                                   _ptr(pos, "pos", (t, top), dev, torch.int32),
+                                   _ptr(p, "p", (t, top), dev, torch.float32), _ptr(out, "out", (t, n), dev),
+                                   _code(out.dtype), _stream(dev)), "vq_expert_combine")
     return out
 
 
@@ -237,22 +259,21 @@ def q8_experts(x, ids, p, w_in, s_in, w_out, s_out, inner, ws, y_dtype=None, out
     """A whole expert layer (vq_q8_experts): x [T, D], ids int32 and p fp32 [T, top], w_in [E, 2 inner, ..] (gate rows
     first), w_out [E, D, ..]; ``ws``: a uint8 device buffer of q8_experts_workspace_bytes."""
     torch = _torch()
-    xp, ld = _rows_ptr(x, "x")
+    xp, ld, code, dev = _rows(x, "x")
     t, d = x.shape
     e = w_in.shape[0]
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, top], got %s" % (tuple(ids.shape),))
     top = ids.shape[1]
-    _expect(ids, "ids", (t, top)), _expect(p, "p", (t, top))
-    _expect(w_in, "w_in", (e, 2 * inner, q8_row_bytes(d))), _expect(s_in, "s_in", (e, 2 * inner))
-    _expect(w_out, "w_out", (e, d, q8_row_bytes(inner))), _expect(s_out, "s_out", (e, d))
-    out = _out(out, (t, d), y_dtype or x.dtype, x.device)
-    _same_device(x, ids=ids, p=p, w_in=w_in, s_in=s_in, w_out=w_out, s_out=s_out, ws=ws, out=out)
-    i8, f32 = (torch.int8,), (torch.float32,)
-    _check(lib().vq_q8_experts(t, top, e, d, inner, xp, _dtype_code(x.dtype), ld, _dev_ptr(ids, "ids", (torch.int32,)),
-                               _dev_ptr(p, "p", f32), _dev_ptr(w_in, "w_in", i8), _dev_ptr(s_in, "s_in", f32),
-                               _dev_ptr(w_out, "w_out", i8), _dev_ptr(s_out, "s_out", f32), _dev_ptr(out, "out"),
-                               _dtype_code(out.dtype), *_ws_args(ws), _stream_ptr(x.device)), "vq_q8_experts")
+    out = _out(out, (t, d), y_dtype or x.dtype, x)
+    i8, f32 = torch.int8, torch.float32
+    _check(lib().vq_q8_experts(t, top, e, d, inner, xp, code, ld, _ptr(ids, "ids", (t, top), dev, torch.int32),
+                               _ptr(p, "p", (t, top), dev, f32),
+                               _ptr(w_in, "w_in", (e, 2 * inner, q8_row_bytes(d)), dev, i8),
+                               _ptr(s_in, "s_in", (e, 2 * inner), dev, f32),
+                               _ptr(w_out, "w_out", (e, d, q8_row_bytes(inner)), dev, i8),
+                               _ptr(s_out, "s_out", (e, d), dev, f32), _ptr(out, "out", (t, d), dev),
+                               _code(out.dtype), *_ws(ws, dev), _stream(dev)), "vq_q8_experts")
     return out
 
 
@@ -270,41 +291,48 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
     torch = _torch()
     if post not in _KINDS or pre not in _KINDS:
         raise ValueError("post and pre must be one of %s" % (tuple(_KINDS),))
-    zp, ldz = _rows_ptr(z, "z")
+    zp, ldz, z_code, dev = _rows(z, "z")
     m, d = z.shape
-    hp, ldh = (None, d) if residual is None else _rows_ptr(residual, "residual")
-    _expect(residual, "residual", (m, d))
-    vecs = [v for v in (post_weight, post_bias, pre_weight, pre_bias) if v is not None]
-    for v in vecs:
-        _expect(v, "a norm weight or bias", (d,))
-        if v.dtype != vecs[0].dtype:
-            raise TypeError("norm weights and biases must share one dtype")
+    hp, ldh, h_code, r_dtype = None, d, z_code, z.dtype
+    if residual is not None:
+        if residual.shape != z.shape:
+            raise ValueError("residual must be %s, got %s" % ([m, d], tuple(residual.shape)))
+        hp, ldh, h_code, h_dev = _rows(residual, "residual")
+        if h_dev != dev:
+            raise ValueError("residual must be on device %d, is on %s" % (dev, residual.device))
+        r_dtype = residual.dtype
+    w_dtype, vecs = None, []
+    for v in (post_weight, post_bias, pre_weight, pre_bias):
+        if v is not None:
+            w_dtype = w_dtype or v.dtype
+            if v.dtype is not w_dtype:
+                raise TypeError("norm weights and biases must share one dtype")
+        vecs.append(_ptr(v, "a norm weight or bias", (d,), dev))
+    gate_p, gate_code = None, VQ_F32
     if gate is not None:
         if gate.dim() == 1:
-            gate, gate_rows = gate.unsqueeze(0), max(m, 1)
-        if gate_rows < 1:
+            gate_rows, shape = max(m, 1), (d,)
+        elif gate_rows < 1:
             raise ValueError("gate_rows must be at least 1, got %d" % gate_rows)
-        _expect(gate, "gate", (-(-m // gate_rows), d))
-    r_dtype = z.dtype if residual is None else residual.dtype
-    r = None
+        else:
+            shape = (-(-m // gate_rows), d)
+        gate_p, gate_code = _ptr(gate, "gate", shape, dev), _code(gate.dtype)
+    r = r_p = None
     if keep_r or r_out is not None:
-        r = _out(r_out, (m, d), r_dtype, z.device)
-    x = q = s = None
+        r = _out(r_out, (m, d), r_dtype, z)
+        r_p = _ptr(r, "r_out", (m, d), dev, r_dtype)
+    x = q = s = x_p = q_p = s_p = None
+    x_code = VQ_F32
     if q8:
-        q = torch.empty((m, q8_row_bytes(d)), dtype=torch.int8, device=z.device)
-        s = torch.empty((m,), dtype=torch.float32, device=z.device)
+        q, s = z.new_empty((m, q8_row_bytes(d)), dtype=torch.int8), z.new_empty((m,), dtype=torch.float32)
+        q_p, s_p = q.data_ptr(), s.data_ptr()
     else:
-        x = torch.empty((m, d), dtype=x_dtype or z.dtype, device=z.device)
-    _same_device(z, residual=residual, post_weight=post_weight, post_bias=post_bias, pre_weight=pre_weight,
-                 pre_bias=pre_bias, gate=gate, r_out=r_out)
-    code = lambda t: VQ_F32 if t is None else _dtype_code(t.dtype)
-    desc = NormDesc(m, d, _KINDS[post], _KINDS[pre], code(z), _dtype_code(r_dtype), code(vecs[0] if vecs else None),
-                    code(gate), code(x), min(int(gate_rows), 2 ** 31 - 1), eps, weight_offset, res_scale, gate_scale,
-                    ldz, ldh)
-    _check(lib().vq_block_norm(ctypes.byref(desc), zp, hp, _dev_ptr(post_weight, "post_weight"),
-                               _dev_ptr(post_bias, "post_bias"), _dev_ptr(pre_weight, "pre_weight"),
-                               _dev_ptr(pre_bias, "pre_bias"), _dev_ptr(gate, "gate"), _dev_ptr(r, "r", (r_dtype,)),
-                               _dev_ptr(x, "x"), _dev_ptr(q, "q"), _dev_ptr(s, "s"), _stream_ptr(z.device)),
+        x = z.new_empty((m, d), dtype=x_dtype or z.dtype)
+        x_p, x_code = x.data_ptr(), _code(x.dtype)
+    desc = NormDesc(m, d, _KINDS[post], _KINDS[pre], z_code, h_code, VQ_F32 if w_dtype is None else _code(w_dtype),
+                    gate_code, x_code, min(int(gate_rows), 2 ** 31 - 1), eps, weight_offset, res_scale, gate_scale, ldz,
+                    ldh)
+    _check(lib().vq_block_norm(ctypes.byref(desc), zp, hp, *vecs, gate_p, r_p, x_p, q_p, s_p, _stream(dev)),
            "vq_block_norm")
     return (r, q, s) if q8 else (r, x)
 
@@ -312,18 +340,34 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
 _stream_ws = {}
 
 
-def _stream_workspace(nbytes, device):
-    """A workspace kept per (device, current stream), grown on demand (None for 0 bytes)."""
-    torch = _torch()
+def _stream_workspace(nbytes, dev, stream):
+    """A workspace kept per (device, stream), grown on demand (None for 0 bytes)."""
     if nbytes == 0:
         return None
-    key = (device.index if device.index is not None else torch.cuda.current_device(),
-           torch.cuda.current_stream(device).cuda_stream)
-    ws = _stream_ws.get(key)
+    ws = _stream_ws.get((dev, stream))
     if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _stream_ws[key] = ws
+        torch = _torch()
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+        _stream_ws[(dev, stream)] = ws
     return ws
+
+
+def _tokens(x):
+    """x [..., K] as rows [M, K] (copied only where its rows are not contiguous)."""
+    if x.dim() != 2:
+        x = x.reshape(-1, x.shape[-1])
+    return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
+
+
+class _Weights:
+    """8-bit weights and what goes with them, checked once: pointers for the calls that follow.  The tensors are held
+    here and not to be replaced."""
+
+    def __init__(self, **named):
+        self.tensors = [t for t, _, _ in named.values() if t is not None]
+        self.dev = _device(self.tensors[0], next(iter(named)))
+        for what, (t, shape, dtype) in named.items():
+            setattr(self, what, _ptr(t, what, shape, self.dev, dtype))
 
 
 class Q8Linear:
@@ -333,8 +377,11 @@ class Q8Linear:
     8 bits already (block_norm, q8_quantize)."""
 
     def __init__(self, w, scale, bias=None):
-        self.out_features, self.in_features = w.shape
+        torch = _torch()
+        n, k = self.out_features, self.in_features = w.shape
         self.w, self.scale, self.bias = q8_pad(w), scale, bias
+        self._p = _Weights(w=(self.w, (n, q8_row_bytes(k)), torch.int8), scale=(scale, (n,), torch.float32),
+                           bias=(bias, (n,), torch.float16))
 
     @classmethod
     def from_weight(cls, w, bias=None):
@@ -343,18 +390,32 @@ class Q8Linear:
         return cls(q[:, :w.shape[1]], s, bias)
 
     def forward(self, x, y_dtype=None):
-        lead = x.shape[:-1]
-        x2 = x.reshape(-1, x.shape[-1])
-        if x2.shape[1] > 1 and x2.stride(1) != 1:
-            x2 = x2.contiguous()
-        ws = _stream_workspace(q8_linear_workspace_bytes(x2.shape[0], self.out_features, self.in_features), x2.device)
-        return q8_linear(x2, self.w, self.scale, self.bias, ws, y_dtype).reshape(*lead, self.out_features)
+        n, k, w = self.out_features, self.in_features, self._p
+        rows = _tokens(x)
+        p, ld, code, dev = _rows(rows, "x")
+        if dev != w.dev or rows.shape[1] != k:
+            raise ValueError("x must be [..., %d] on device %d, got %s on %s" % (k, w.dev, tuple(x.shape), x.device))
+        m, stream = rows.shape[0], _stream(dev)
+        y = rows.new_empty((m, n), dtype=y_dtype or x.dtype)
+        nbytes = q8_linear_workspace_bytes(m, n, k)
+        ws = _stream_workspace(nbytes, dev, stream)
+        _check(lib().vq_q8_linear(m, n, k, p, code, ld, w.w, w.scale, w.bias, y.data_ptr(), _code(y.dtype),
+                                  None if ws is None else ws.data_ptr(), nbytes, stream), "vq_q8_linear")
+        return y if x.dim() == 2 else y.reshape(*x.shape[:-1], n)
 
     __call__ = forward
 
     def forward_q8(self, q, s, y_dtype=None):
-        ws = _stream_workspace(q8_gemm_workspace_bytes(q.shape[0], self.out_features, self.in_features), q.device)
-        return q8_gemm(q, s, self.w, self.scale, self.bias, self.in_features, ws, y_dtype)
+        torch = _torch()
+        n, k, w = self.out_features, self.in_features, self._p
+        m, stream = q.shape[0], _stream(w.dev)
+        y = q.new_empty((m, n), dtype=y_dtype or torch.bfloat16)
+        nbytes = q8_gemm_workspace_bytes(m, n, k)
+        ws = _stream_workspace(nbytes, w.dev, stream)
+        _check(lib().vq_q8_gemm(m, n, k, _ptr(q, "q", (m, q8_row_bytes(k)), w.dev, torch.int8),
+                                _ptr(s, "s", (m,), w.dev, torch.float32), w.w, w.scale, w.bias, y.data_ptr(),
+                                _code(y.dtype), None if ws is None else ws.data_ptr(), nbytes, stream), "vq_q8_gemm")
+        return y
 
 
 class Q8Experts:
@@ -362,18 +423,33 @@ class Q8Experts:
     s_in [E, 2 I] and s_out [E, D]."""
 
     def __init__(self, w_in, s_in, w_out, s_out):
-        self.experts, self.inner = w_in.shape[0], w_out.shape[2]
+        torch = _torch()
+        e, d, i = w_out.shape
+        self.experts, self.features, self.inner = e, d, i
         self.w_in, self.s_in, self.w_out, self.s_out = q8_pad(w_in), s_in, q8_pad(w_out), s_out
+        self._p = _Weights(w_in=(self.w_in, (e, 2 * i, q8_row_bytes(d)), torch.int8),
+                           s_in=(s_in, (e, 2 * i), torch.float32),
+                           w_out=(self.w_out, (e, d, q8_row_bytes(i)), torch.int8),
+                           s_out=(s_out, (e, d), torch.float32))
 
     def forward(self, x, ids, p, y_dtype=None):
         """y [..., D] for x [..., D] and its tokens' expert ids (int32) and weights (fp32) [tokens, top]."""
-        lead = x.shape[:-1]
-        x2 = x.reshape(-1, x.shape[-1])
-        if x2.shape[1] > 1 and x2.stride(1) != 1:
-            x2 = x2.contiguous()
-        ws = _stream_workspace(q8_experts_workspace_bytes(x2.shape[0], ids.shape[1], self.experts, x2.shape[1],
-                                                          self.inner), x2.device)
-        y = q8_experts(x2, ids, p, self.w_in, self.s_in, self.w_out, self.s_out, self.inner, ws, y_dtype)
-        return y.reshape(*lead, x2.shape[1])
+        torch = _torch()
+        e, d, i, w = self.experts, self.features, self.inner, self._p
+        rows = _tokens(x)
+        xp, ld, code, dev = _rows(rows, "x")
+        if dev != w.dev or rows.shape[1] != d:
+            raise ValueError("x must be [..., %d] on device %d, got %s on %s" % (d, w.dev, tuple(x.shape), x.device))
+        if ids.dim() != 2:
+            raise ValueError("ids must be [tokens, top], got %s" % (tuple(ids.shape),))
+        t, top, stream = rows.shape[0], ids.shape[1], _stream(dev)
+        y = rows.new_empty((t, d), dtype=y_dtype or x.dtype)
+        nbytes = q8_experts_workspace_bytes(t, top, e, d, i)
+        ws = _stream_workspace(nbytes, dev, stream)
+        _check(lib().vq_q8_experts(t, top, e, d, i, xp, code, ld, _ptr(ids, "ids", (t, top), dev, torch.int32),
+                                   _ptr(p, "p", (t, top), dev, torch.float32), w.w_in, w.s_in, w.w_out, w.s_out,
+                                   y.data_ptr(), _code(y.dtype), None if ws is None else ws.data_ptr(), nbytes, stream),
+               "vq_q8_experts")
+        return y if x.dim() == 2 else y.reshape(*x.shape[:-1], d)
 
     __call__ = forward
