@@ -201,6 +201,26 @@ struct Q8Args {
 int32_t q8_splits(int32_t m, int32_t n, int32_t k);
 vq_status launch_q8(const Q8Args& a, void* stream);
 
+// Products of one token that is cut to 8 bits inside the kernel (vq_q8.hip): dense (experts == 0), the gated products of
+// its `slots` experts (y fp32 [slots][n], x one row), or their joined outputs (join: x fp32 [slots][k], y [n]).
+struct OneArgs {
+  int32_t n, k, slots, experts;
+  const void* x;
+  vq_dtype x_dtype;
+  const uint8_t* w;
+  const float* sw;
+  const uint16_t* bias;  // dense only
+  const int32_t* ids;    // [slots]
+  const float* p;        // [slots]
+  int32_t gated, join;
+  void* y;
+  vq_dtype y_dtype;
+};
+constexpr int32_t kQ8OneSlots = 8;            // most slots of the joined form
+constexpr size_t kQ8OneLds = 63 * 1024;       // most dynamic LDS of a workgroup
+size_t q8_one_lds(const OneArgs& a);
+vq_status launch_q8_one(const OneArgs& a, void* stream);
+
 // Routing (vq_experts.hip): ids [tokens * top] -> offsets [experts + 1], rows and pos [tokens * top].
 vq_status launch_expert_plan(int32_t tokens, int32_t top, int32_t experts, const int32_t* ids, int32_t* offsets,
                              int32_t* rows, int32_t* pos, void* stream);

@@ -3,12 +3,17 @@
 //
 // Rows of q and w are whole 128-byte steps with zero pads, so no kernel has a K edge; rows past an edge of a tile read
 // the last valid row again and are not stored.  Sums of integers have no order, so nothing here depends on how K is cut.
+#include <algorithm>
+
 #include "vq_device.h"
 #include "vq_q8_device.h"
 
 namespace {
 
+using vqi::OneArgs;
 using vqi::Q8Args;
+
+constexpr int kOneSlots = vqi::kQ8OneSlots;
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
@@ -68,7 +73,18 @@ __device__ __forceinline__ int32_t token_of(const Q8Args& a, int32_t r) {
   return a.rows ? min(max(a.rows[r], 0), a.tokens - 1) : min(r, a.tokens - 1);
 }
 
-__device__ __forceinline__ float silu(float g) { return g * (1.0f / (1.0f + expf(-g))); }
+// g / (1 + exp(-g)) to about 3 ulp.  exp(-g) = 2^h (1 + l ln 2), where h is -g log2(e) rounded and l what the rounding
+// left (log2(e) itself in two parts): the hardware's 2^h alone would lose an ulp for every unit of |h|, and those
+// decide which way a hidden value's 8-bit rounding falls.  Past +-200 the sigmoid is 0 or 1 in fp32, and infinities stay
+// out of the remainder; a NaN comes back through the last product.
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kL = 0x1.715476p+0f, kLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;  // log2(e) = kL + kLow
+  const float c = -__builtin_amdgcn_fmed3f(g, -200.0f, 200.0f);
+  const float h = c * kL;
+  const float l = __builtin_fmaf(c, kLow, __builtin_fmaf(c, kL, -h));
+  const float e = __builtin_amdgcn_exp2f(h) * __builtin_fmaf(l, kLn2, 1.0f);
+  return g * __builtin_amdgcn_rcpf(1.0f + e);
+}
 
 // Stores CNT consecutive outputs of one row from column n on (those below n_end), as one block where it is whole.
 template <int CNT>
@@ -113,40 +129,21 @@ __device__ __forceinline__ void to_lds(const uint8_t* g, uint8_t* l) {
                                    (__attribute__((address_space(3))) void*)l, 16, 0, 0);
 }
 
-// A workgroup of WM x WN wavefronts computes BM tokens x BN weight rows (with the gate: BN / 2 outputs, 32-row blocks of
-// gate and up rows in turn, so that a lane ends with both values of an output).  The weights are the matrix
-// instruction's first operand: a lane then holds 16 outputs of one token, and since block row i holds weight row
-// perm(i) they are 16 consecutive ones.
+// One tile: WM x WN wavefronts compute BM rows (from row0, those below end) by BN weight rows (with the gate: BN / 2
+// outputs, 32-row blocks of gate and up rows in turn, so that a lane ends with both values of an output).  The weights
+// are the matrix instruction's first operand: a lane then holds 16 outputs of one token, and since block row i holds
+// weight row perm(i) they are 16 consecutive ones.
 template <int BM, int BN, int WM, int WN, bool GATED, bool SPLIT>
-__global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t nt, int32_t mt_count) {
+__device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0, uint8_t* lds) {
   constexpr int kWaves = WM * WN;
   constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
   constexpr int TL = BM / 8 / kWaves, WL = BN / 8 / kWaves;  // 8-row loads per wavefront and step
+  constexpr int kBuf = (BM + BN) * kStep;
   static_assert(TL * 8 * kWaves == BM && WL * 8 * kWaves == BN, "whole loads");
   static_assert(!GATED || NI % 2 == 0, "gate and up blocks in one wavefront");
-  constexpr int kOut = GATED ? BN / 2 : BN;  // outputs per tile
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][(BM + BN) * kStep];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-  // tiles of one XCD (workgroup mod 8) are neighbours: 8 row tiles by all columns, columns slowest
-  const int32_t total = mt_count * nt;
-  const int32_t per = (total + 7) / 8;
-  const int32_t id = (int32_t)(blockIdx.x & 7) * per + (int32_t)(blockIdx.x >> 3);
-  if ((int32_t)(blockIdx.x >> 3) >= per || id >= total) return;
-  const int32_t band = id / (8 * nt), in_band = id - band * 8 * nt;
-  const int32_t band_rows = min(8, mt_count - band * 8);
-  const int32_t mt = band * 8 + in_band % band_rows;
-  const int32_t n0 = in_band / band_rows * kOut;
-
-  Span sp{0, 0, 0};
-  if (a.experts) {
-    if (!find_span<BM>(a, mt, sp)) return;
-  } else {
-    sp.row0 = mt * BM;
-    sp.end = a.m;
-  }
   const int64_t ld = vqi::q8_row_bytes(a.k);
   const int64_t wrows = GATED ? 2 * (int64_t)a.n : a.n;
   const uint8_t* const w = a.w + (int64_t)sp.e * wrows * ld;
@@ -184,12 +181,12 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t
   auto fetch = [&](int buf) {
 #pragma unroll
     for (int j = 0; j < TL; ++j) {
-      to_lds(gt[j], &lds[buf][(j * kWaves + wave) * 1024]);
+      to_lds(gt[j], lds + buf * kBuf + (j * kWaves + wave) * 1024);
       gt[j] += kStep;
     }
 #pragma unroll
     for (int j = 0; j < WL; ++j) {
-      to_lds(gw[j], &lds[buf][BM * kStep + (j * kWaves + wave) * 1024]);
+      to_lds(gw[j], lds + buf * kBuf + BM * kStep + (j * kWaves + wave) * 1024);
       gw[j] += kStep;
     }
   };
@@ -204,31 +201,53 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
+  // fragments of one 32-byte slice of the step, two sets: the next slice is read while this one is multiplied
   const int lt = (wm * MI * 32 + col) * kStep;
   const int lw = BM * kStep + (wn * NI * 32 + col) * kStep;
-  auto multiply = [&](int buf) {
+  v4i ft[2][MI], fw[2][NI];
+  auto read = [&](int set, int buf, int ks) {
+    const int c = ((2 * ks + half) ^ ((lane >> 1) & 7)) * 16;
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const int c = ((2 * ks + half) ^ ((lane >> 1) & 7)) * 16;
-      v4i t[MI], v[NI];
+    for (int i = 0; i < MI; ++i) ft[set][i] = *(const v4i*)(lds + buf * kBuf + lt + i * 32 * kStep + c);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) t[i] = *(const v4i*)&lds[buf][lt + i * 32 * kStep + c];
+    for (int j = 0; j < NI; ++j) fw[set][j] = *(const v4i*)(lds + buf * kBuf + lw + j * 32 * kStep + c);
+  };
+  auto multiply = [&](int set) {
 #pragma unroll
-      for (int j = 0; j < NI; ++j) v[j] = *(const v4i*)&lds[buf][lw + j * 32 * kStep + c];
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(v[j], t[i], acc[i][j], 0, 0, 0);
-    }
+      for (int j = 0; j < NI; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][j], ft[set][i], acc[i][j], 0, 0, 0);
   };
 
   fetch(0);
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wavefront's part of the first step is in LDS
+  __syncthreads();                     // and everyone's
+  if (kt0 + 1 < kt1) fetch(1);
+  read(0, 0, 0);
   int buf = 0;
   for (int32_t kt = kt0; kt < kt1; ++kt) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wavefront's part of step kt is in LDS
-    __syncthreads();                     // everyone's is, and the other buffer's readers are done
-    if (kt + 1 < kt1) fetch(buf ^ 1);
-    multiply(buf);
+    read(1, buf, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(0);
+    __builtin_amdgcn_sched_barrier(0);
+    read(0, buf, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1);
+    __builtin_amdgcn_sched_barrier(0);
+    read(1, buf, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (kt + 1 < kt1) {
+      __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): its part of the next step is in LDS, its last reads are done
+      __syncthreads();                     // and everyone's: the next step may be read, this one overwritten
+      if (kt + 2 < kt1) fetch(buf);
+      read(0, buf ^ 1, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    multiply(1);
+    __builtin_amdgcn_sched_barrier(0);
     buf ^= 1;
   }
 
@@ -261,11 +280,22 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t
           float g[16], u[16], bg[16], bu[16], v[16];
           load_run<16>(sw, n, a.n, g);
           load_run<16>(sw + a.n, n, a.n, u);
-          load_bias<16>(bias, n, a.n, bg);
-          load_bias<16>(bias ? bias + a.n : nullptr, n, a.n, bu);
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            v[r] = silu((float)acc[i][j][r] * s * g[r] + bg[r]) * ((float)acc[i][j + 1][r] * s * u[r] + bu[r]);
+          for (int r = 0; r < 16; ++r) {
+            g[r] *= (float)acc[i][j][r] * s;
+            u[r] *= (float)acc[i][j + 1][r] * s;
+          }
+          if (bias) {
+            load_bias<16>(bias, n, a.n, bg);
+            load_bias<16>(bias + a.n, n, a.n, bu);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              g[r] += bg[r];
+              u[r] += bu[r];
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] = silu(g[r]) * u[r];
           store_run<16>(a.y, a.y_dtype, (int64_t)m * a.n, n, a.n, v);
         }
       } else {
@@ -281,6 +311,62 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t
         }
       }
     }
+  }
+}
+
+// Tiles of one XCD (workgroup mod 8) are neighbours: 8 row tiles by all columns, columns slowest.  false: no such tile.
+__device__ __forceinline__ bool place(int32_t id, int32_t total, int32_t mt_count, int32_t nt, int32_t& mt, int32_t& nti) {
+  const int32_t per = (total + 7) / 8;
+  const int32_t at = (id & 7) * per + (id >> 3);
+  if ((id >> 3) >= per || at >= total) return false;
+  const int32_t band = at / (8 * nt), in_band = at - band * 8 * nt;
+  const int32_t band_rows = min(8, mt_count - band * 8);
+  mt = band * 8 + in_band % band_rows;
+  nti = in_band / band_rows;
+  return true;
+}
+
+// Tiles with several workgroups per CU.
+template <int BM, int BN, int WM, int WN, bool GATED, bool SPLIT>
+__global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t nt, int32_t mt_count) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (BM + BN) * kStep];
+  int32_t mt, nti;
+  if (!place((int32_t)blockIdx.x, mt_count * nt, mt_count, nt, mt, nti)) return;
+  Span sp{0, mt * BM, a.m};
+  if (a.experts && !find_span<BM>(a, mt, sp)) return;
+  tile<BM, BN, WM, WN, GATED, SPLIT>(a, sp, nti * (GATED ? BN / 2 : BN), lds);
+}
+
+// 256 x 256 tiles on 8 wavefronts, one workgroup per CU: half the LDS reads and a third fewer matrix bytes per operation
+// than 128 x 128.  Tiles of 128 rows where a group's (or the matrix's) last tile has no more left, and for the tiles from
+// `full` on, which are the last, partial round over the CUs: two half tiles there take one round of half the length.
+template <bool GATED>
+__global__ __launch_bounds__(512) void q8_big_kernel(Q8Args a, int32_t nt, int32_t mt_count, int32_t full) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * 512 * kStep];
+  const int32_t out = GATED ? 128 : 256;
+  int32_t mt, nti, part = 0;
+  const int32_t id = (int32_t)blockIdx.x;
+  const bool half = id >= full;
+  if (!half) {
+    if (!place(id, min(full, mt_count * nt), mt_count, nt, mt, nti)) return;
+  } else {
+    const int32_t at = full + (id - full) / 2;
+    if (at >= mt_count * nt) return;
+    part = (id - full) & 1;
+    const int32_t band = at / (8 * nt), in_band = at - band * 8 * nt;
+    const int32_t band_rows = min(8, mt_count - band * 8);
+    mt = band * 8 + in_band % band_rows;
+    nti = in_band / band_rows;
+  }
+  Span sp{0, mt * 256, a.m};
+  if (a.experts && !find_span<256>(a, mt, sp)) return;
+  sp.row0 += part * 128;
+  if (sp.row0 >= sp.end) return;
+  if (half) sp.end = min(sp.end, sp.row0 + 128);
+  if (half || sp.end - sp.row0 <= 128) {
+    tile<128, 256, 2, 4, GATED, false>(a, sp, nti * out, lds);
+  } else {
+    tile<256, 256, 2, 4, GATED, false>(a, sp, nti * out, lds);
   }
 }
 
@@ -316,43 +402,32 @@ __global__ __launch_bounds__(256) void q8_join_kernel(Q8Args a) {
 // ---------------------------------------------------------------- few rows
 
 // Few tokens: the weights are read once, straight into the matrix instruction's registers.  A workgroup of 8 wavefronts
-// takes RT blocks of 16 weight rows (with the gate: 8 RT outputs, one block of gate rows and one of up rows) and up to
-// 16 MT tokens; its wavefronts cut K, their int32 sums meet in LDS.
-template <int RT, int MT, bool GATED>
+// takes WN x RT blocks of 16 weight rows and up to 16 MT tokens; the WK = 8 / WN wavefronts of a row block cut K, their
+// int32 sums meet in LDS.
+template <int RT, int MT, int WN>
 __global__ __launch_bounds__(512) void q8_few_kernel(Q8Args a) {
-  constexpr int kWaves = 8;
+  constexpr int WK = 8 / WN;
   constexpr int kTiles = RT * MT;
-  constexpr int U = 4;  // 64-byte steps in flight
-  static_assert(!GATED || RT == 2, "one gate block and one up block");
-  constexpr int kOut = GATED ? 16 : 16 * RT;
-  __shared__ v4i red[kWaves][kTiles][64];
+  constexpr int U = RT * MT == 1 ? 8 : RT * MT <= 6 ? 4 : 2;  // 64-byte steps in flight
+  __shared__ v4i red[8][kTiles][64];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t n0 = (int32_t)blockIdx.x * kOut;
-  Span sp{0, 0, 0};
-  if (a.experts) {
-    if (!find_span<16 * MT>(a, (int32_t)blockIdx.y, sp)) return;
-  } else {
-    sp.row0 = (int32_t)blockIdx.y * 16 * MT;
-    sp.end = a.m;
-  }
+  const int wk = wave % WK, wn = wave / WK;
+  const int32_t n0 = ((int32_t)blockIdx.x * WN + wn) * 16 * RT;
   const int64_t ld = vqi::q8_row_bytes(a.k);
-  const int64_t wrows = GATED ? 2 * (int64_t)a.n : a.n;
   const int32_t steps = (int32_t)(ld / 64);
-  const int32_t k0 = steps * wave / kWaves, k1 = steps * (wave + 1) / kWaves;
+  const int32_t k0 = steps * wk / WK, k1 = steps * (wk + 1) / WK;
   const int row = lane & 15, grp = lane >> 4;
 
   const uint8_t* gw[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int64_t r = GATED ? (int64_t)min(n0 + row, a.n - 1) + (i ? a.n : 0) : min(n0 + 16 * i + row, a.n - 1);
-    gw[i] = a.w + ((int64_t)sp.e * wrows + r) * ld + (int64_t)k0 * 64 + grp * 16;
-  }
+  for (int i = 0; i < RT; ++i)
+    gw[i] = a.w + (int64_t)min(n0 + 16 * i + row, a.n - 1) * ld + (int64_t)k0 * 64 + grp * 16;
   const uint8_t* gt[MT];
 #pragma unroll
   for (int j = 0; j < MT; ++j)
-    gt[j] = a.q + (int64_t)token_of(a, min(sp.row0 + 16 * j + row, sp.end - 1)) * ld + (int64_t)k0 * 64 + grp * 16;
+    gt[j] = a.q + (int64_t)min(16 * j + row, a.m - 1) * ld + (int64_t)k0 * 64 + grp * 16;
 
   v4i acc[RT][MT];
 #pragma unroll
@@ -374,6 +449,7 @@ __global__ __launch_bounds__(512) void q8_few_kernel(Q8Args a) {
     for (int i = 0; i < RT; ++i) gw[i] += 64 * U;
 #pragma unroll
     for (int j = 0; j < MT; ++j) gt[j] += 64 * U;
+    __builtin_amdgcn_sched_barrier(0);  // all U steps' loads are in flight before the first is used
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -402,46 +478,282 @@ __global__ __launch_bounds__(512) void q8_few_kernel(Q8Args a) {
     for (int j = 0; j < MT; ++j) red[wave][i * MT + j][lane] = acc[i][j];
   __syncthreads();
 
-  // lane: token lane % 16, channels 4 (lane / 16) .. + 3 of a block
-  const float* sw = a.sw + (int64_t)sp.e * wrows;
-  const uint16_t* bias = a.bias ? a.bias + (int64_t)sp.e * wrows : nullptr;
-  for (int o = wave; o < (GATED ? MT : kTiles); o += kWaves) {
+  // lane: token lane % 16, channels 4 (lane / 16) .. + 3 of a block; the WK wavefronts share the blocks out
+  for (int o = wk; o < kTiles; o += WK) {
     const int j = o % MT, i = o / MT;
-    const int32_t m = sp.row0 + 16 * j + row;
+    const int32_t m = 16 * j + row;
     const int32_t n = n0 + 16 * i + 4 * grp;
-    v4i sum = red[0][o][lane], up = v4i{0, 0, 0, 0};
+    v4i sum = red[wn * WK][o][lane];
 #pragma unroll
-    for (int k = 1; k < kWaves; ++k) sum += red[k][o][lane];
-    if constexpr (GATED) {
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) up += red[k][MT + o][lane];
-    }
-    if (m >= sp.end) continue;
-    const float s = a.s[token_of(a, m)];
+    for (int v = 1; v < WK; ++v) sum += red[wn * WK + v][o][lane];
+    if (m >= a.m) continue;
+    const float s = a.s[m];
     float sc[4], b[4], v[4];
-    load_run<4>(sw, n, a.n, sc);
-    load_bias<4>(bias, n, a.n, b);
+    load_run<4>(a.sw, n, a.n, sc);
+    load_bias<4>(a.bias, n, a.n, b);
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] = (float)sum[r] * s * sc[r] + b[r];
-    if constexpr (GATED) {
-      load_run<4>(sw + a.n, n, a.n, sc);
-      load_bias<4>(bias ? bias + a.n : nullptr, n, a.n, b);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = silu(v[r]) * ((float)up[r] * s * sc[r] + b[r]);
-    }
     store_run<4>(a.y, a.y_dtype, (int64_t)m * a.n, n, a.n, v);
+  }
+}
+
+// ---------------------------------------------------------------- one token
+
+// Products of a single token, cut to 8 bits inside the kernel: each workgroup finds the row's scale (of the 1 + rows it
+// needs: `slots`) and keeps the 8-bit row in LDS while its first weight loads are on their way, so a token costs one
+// launch.  Weights go to the matrix instruction as in q8_few_kernel, with the token in all 16 columns.
+//   dense   y = the product                                        w [n]
+//   GATED   slot blockIdx.y: y[slot] = silu(g) u, fp32             w [experts][2 n], expert ids[slot], the same x for all
+//   JOIN    y = sum over slots of p[slot] * product(x row slot)    w [experts][n], experts ids[slot]
+// Slots whose id is outside [0, experts) are left out.
+template <int RT, int WN, bool GATED, bool JOIN, vq_dtype XT>
+__global__ __launch_bounds__(512) void q8_one_kernel(OneArgs a) {
+  constexpr int WK = 8 / WN;
+  constexpr int U = RT == 1 ? 8 : 4;  // 64-byte steps in flight
+  constexpr int kOut = GATED ? 16 : 16 * RT;
+  static_assert(!GATED || RT == 2, "one gate block and one up block");
+  static_assert(!JOIN || RT == 1, "one block per wavefront");
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ uint32_t big[8][kOneSlots];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wk = wave % WK, wn = wave / WK;
+  const int32_t n0 = ((int32_t)blockIdx.x * WN + wn) * kOut;
+  const int64_t ld = vqi::q8_row_bytes(a.k);
+  const int64_t wrows = GATED ? 2 * (int64_t)a.n : a.n;
+  const int slots = JOIN ? a.slots : 1;
+  const int32_t first = JOIN ? 0 : (int32_t)blockIdx.y;  // the slot (GATED) or the first slot
+  auto expert = [&](int slot) { return a.experts ? a.ids[slot] : 0; };
+  auto there = [&](int32_t e) { return a.experts == 0 || (e >= 0 && e < a.experts); };
+  if (!JOIN && !there(expert(first))) return;
+
+  const int32_t steps = (int32_t)(ld / 64);
+  const int32_t k0 = steps * wk / WK, k1 = steps * (wk + 1) / WK;
+  const int row = lane & 15, grp = lane >> 4;
+  const uint8_t* gw[RT];
+  auto aim = [&](int32_t e) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int64_t r = GATED ? (int64_t)min(n0 + row, a.n - 1) + (i ? a.n : 0) : min(n0 + 16 * i + row, a.n - 1);
+      gw[i] = a.w + ((int64_t)e * wrows + r) * ld + (int64_t)k0 * 64 + grp * 16;
+    }
+  };
+  v4i w[2][U][RT];  // two blocks of U steps: one on its way while the other is used
+  auto load = [&](int set) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) w[set][u][i] = __builtin_nontemporal_load((const v4i*)(gw[i] + 64 * u));
+#pragma unroll
+    for (int i = 0; i < RT; ++i) gw[i] += 64 * U;
+  };
+  const int32_t blocks = (k1 - k0) / U;  // whole blocks of U steps; the steps left over are loaded one by one
+  // the first slot that has an expert; its first loads
+  int slot = 0;
+  while (JOIN && slot < slots && !there(expert(slot))) ++slot;
+  if (slot < slots) {
+    aim(expert(first + slot));
+    if (blocks > 0) load(0);
+    if (blocks > 1) load(1);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+
+  // the rows' largest values, then the rows in 8 bits
+  const int64_t xrow = JOIN ? a.k : 0;  // GATED slots share the token's row
+  auto chunk = [&](int j, int32_t c, float (&f)[8]) {
+    constexpr int es = XT == VQ_F32 ? 4 : 2;
+    const char* p = (const char*)a.x + (j * xrow + (int64_t)c * 8) * es;
+    if (c * 8 + 8 <= a.k) {
+      uint32_t v[2 * es];
+      __builtin_memcpy(v, p, 8 * es);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (XT == VQ_F32) {
+          f[k] = __builtin_bit_cast(float, v[k]);
+        } else {
+          f[k] = vqd::x_to_f32<XT == VQ_F16 ? 0 : 1>(v[k / 2] >> (16 * (k & 1)));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        f[k] = 0.f;
+        if (c * 8 + k < a.k) {
+          if constexpr (XT == VQ_F32) {
+            f[k] = ((const float*)p)[k];
+          } else {
+            f[k] = vqd::x_to_f32<XT == VQ_F16 ? 0 : 1>(((const uint16_t*)p)[k]);
+          }
+        }
+      }
+    }
+  };
+  const int32_t chunks = (a.k + 7) / 8;
+  constexpr int kHold = JOIN ? 1 : 2;  // chunks per thread that stay in registers between the two sweeps
+  float hold[kHold][8];
+  for (int j = 0; j < slots; ++j) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+      const int32_t c = threadIdx.x + 512 * h;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) hold[h][k] = 0.f;
+      if (c < chunks) chunk(j, c, hold[h]);
+    }
+#pragma unroll
+    for (int h = 0; h < kHold; ++h)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max(m, vqd::abs_bits(hold[h][k]));
+    for (int32_t c = threadIdx.x + 512 * kHold; c < chunks; c += 512) {
+      float f[8];
+      chunk(j, c, f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max(m, vqd::abs_bits(f[k]));
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+    if (lane == 0) big[wave][j] = m;
+  }
+  __syncthreads();
+  auto scale = [&](int j) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) m = max(m, big[v][j]);
+    return vqd::q8_scale(m);
+  };
+  for (int j = 0; j < slots; ++j) {
+    const vqd::Q8Scale sc = scale(j);
+    auto put = [&](int32_t c, const float (&f)[8]) {
+      uint32_t v[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k >> 2] |= (uint32_t)(uint8_t)vqd::q8_value(f[k], sc) << (8 * (k & 3));
+      *(uint2*)(lds + j * ld + c * 8) = make_uint2(v[0], v[1]);
+    };
+    int32_t c = threadIdx.x;
+    if (!JOIN) {
+#pragma unroll
+      for (int h = 0; h < kHold; ++h, c += 512)
+        if (c * 8 < (int32_t)ld) put(c, hold[h]);  // zeros past the row's end
+    }
+    for (; c * 8 < (int32_t)ld; c += 512) {
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (c < chunks) chunk(j, c, f);
+      put(c, f);
+    }
+  }
+  __syncthreads();
+
+  v4i* const red = (v4i*)(lds + slots * ld);  // [slots][8][RT][64]
+  for (; slot < slots;) {
+    v4i acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = v4i{0, 0, 0, 0};
+    const uint8_t* xq = lds + slot * ld + (int64_t)k0 * 64 + grp * 16;
+    int next = slot + 1;
+    while (JOIN && next < slots && !there(expert(next))) ++next;
+    auto use = [&](int set) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const v4i t = *(const v4i*)(xq + 64 * u);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[set][u][i], t, acc[i], 0, 0, 0);
+      }
+      xq += 64 * U;
+    };
+    for (int32_t k = 0; k < blocks; k += 2) {
+      use(0);
+      if (k + 2 < blocks) load(0);
+      if (k + 1 < blocks) {
+        use(1);
+        if (k + 3 < blocks) load(1);
+      }
+    }
+    for (int32_t k = k0 + blocks * U; k < k1; ++k, xq += 64) {
+      const v4i t = *(const v4i*)xq;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const v4i v = __builtin_nontemporal_load((const v4i*)gw[i]);
+        gw[i] += 64;
+        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, t, acc[i], 0, 0, 0);
+      }
+    }
+    if (JOIN && next < slots) {  // the next slot's weights are on their way while this one's sums are put down
+      aim(expert(next));
+      if (blocks > 0) load(0);
+      if (blocks > 1) load(1);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) red[((slot * 8 + wave) * RT + i) * 64 + lane] = acc[i];
+    slot = next;
+  }
+  __syncthreads();
+
+  // lane: column lane % 16 (all alike), channels 4 (lane / 16) .. + 3 of a block: column 0 writes
+  if (row != 0) return;
+  auto total = [&](int j, int i) {
+    v4i sum = v4i{0, 0, 0, 0};
+#pragma unroll
+    for (int v = 0; v < WK; ++v) sum += red[((j * 8 + wn * WK + v) * RT + i) * 64 + lane];
+    return sum;
+  };
+  if constexpr (JOIN) {
+    if (wk != 0) return;
+    const int32_t n = n0 + 4 * grp;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < slots; ++j) {
+      const int32_t e = expert(j);
+      if (!there(e)) continue;
+      const v4i sum = total(j, 0);
+      const float s = scale(j).s, p = a.p[j];
+      float sc[4];
+      load_run<4>(a.sw + (int64_t)e * wrows, n, a.n, sc);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(p, (float)sum[r] * s * sc[r], y[r]);
+    }
+    store_run<4>(a.y, a.y_dtype, 0, n, a.n, y);
+  } else {
+    const float s = scale(0).s;
+    const float* sw = a.sw + (int64_t)expert(first) * wrows;
+    for (int i = wk; i < (GATED ? 1 : RT); i += WK) {
+      const int32_t n = n0 + 16 * i + 4 * grp;
+      const v4i sum = total(0, i);
+      float sc[4], b[4], v[4];
+      load_run<4>(sw, n, a.n, sc);
+      load_bias<4>(a.bias, n, a.n, b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = (float)sum[r] * s * sc[r] + b[r];
+      if constexpr (GATED) {
+        const v4i up = total(0, 1);
+        load_run<4>(sw + a.n, n, a.n, sc);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = silu(v[r]) * ((float)up[r] * s * sc[r]);
+      }
+      store_run<4>(a.y, a.y_dtype, (int64_t)first * a.n, n, a.n, v);
+    }
   }
 }
 
 // ---------------------------------------------------------------- launches
 
-template <int RT, int MT, bool GATED>
+// Weight rows per workgroup of the kernels that stream the weights: 64, 32 or 16, as many as leave most CUs a workgroup.
+// One token, 14336 x 4096: 15.9 us with 64 rows, 16.9 with 32 and 18.1 with 16; 4096 x 4096: 13.9, 9.2 and 8.4 us.
+inline int rows_per_group(int32_t n) { return n / 64 >= 192 ? 64 : n / 32 > 144 ? 32 : 16; }
+
+template <int RT, int MT, int WN>
 vq_status launch_few(const Q8Args& a, hipStream_t st) {
-  const int out = GATED ? 16 : 16 * RT;
-  const int64_t gy = a.experts ? span_bound(a, 16 * MT) : ((int64_t)a.m + 16 * MT - 1) / (16 * MT);
-  if (gy > 65535 || !vqi::grid_ok((a.n + out - 1) / out, 512)) return VQ_ERR_SHAPE;
-  q8_few_kernel<RT, MT, GATED><<<dim3((uint32_t)((a.n + out - 1) / out), (uint32_t)gy), dim3(512), 0, st>>>(a);
+  const int64_t blocks = ((int64_t)a.n + WN * RT * 16 - 1) / (WN * RT * 16);
+  if (!vqi::grid_ok(blocks, 512)) return VQ_ERR_SHAPE;
+  q8_few_kernel<RT, MT, WN><<<dim3((uint32_t)blocks), dim3(512), 0, st>>>(a);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
+}
+template <int MT>
+vq_status launch_few_rows(const Q8Args& a, hipStream_t st) {
+  switch (rows_per_group(a.n)) {
+    case 64: return launch_few<2, MT, 2>(a, st);
+    case 32: return launch_few<2, MT, 1>(a, st);
+    default: return launch_few<1, MT, 1>(a, st);
+  }
 }
 
 template <int BM, int BN, int WM, int WN, bool GATED, bool SPLIT>
@@ -449,52 +761,123 @@ vq_status launch_tile(const Q8Args& a, hipStream_t st) {
   const int out = GATED ? BN / 2 : BN;
   const int64_t mt = a.experts ? span_bound(a, BM) : ((int64_t)a.m + BM - 1) / BM;
   const int64_t nt = ((int64_t)a.n + out - 1) / out;
-  if (mt * nt > 0x3FFFFFFF || !vqi::grid_ok(mt * nt + 8, 64 * WM * WN)) return VQ_ERR_SHAPE;
+  if (!vqi::grid_ok(mt * nt + 8, 64 * WM * WN)) return VQ_ERR_SHAPE;
   const uint32_t blocks = (uint32_t)((mt * nt + 7) / 8 * 8);
   q8_tile_kernel<BM, BN, WM, WN, GATED, SPLIT>
       <<<dim3(blocks, SPLIT ? a.splits : 1), dim3(64 * WM * WN), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
 }
-
-constexpr int kFewRows = 64;  // rows (of a group, on average) up to which the weights are streamed through registers
+vq_status launch_join(const Q8Args& a, hipStream_t st) {
+  const int64_t items = (int64_t)a.m * ((a.n + 3) / 4);  // under 256 tiles of 128 x 128: a small grid
+  q8_join_kernel<<<dim3((uint32_t)((items + 255) / 256)), dim3(256), 0, st>>>(a);
+  return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
+}
+template <bool GATED>
+vq_status launch_big(const Q8Args& a, hipStream_t st) {
+  const int out = GATED ? 128 : 256;
+  const int64_t mt = a.experts ? span_bound(a, 256) : ((int64_t)a.m + 255) / 256;
+  const int64_t nt = ((int64_t)a.n + out - 1) / out;
+  if (!vqi::grid_ok(2 * mt * nt + 8, 512)) return VQ_ERR_SHAPE;
+  // whole rounds of 256 tiles, then the rest in halves where they fit one round; a grouped product's tiles are a bound,
+  // so its last round is not known here
+  int64_t full = mt * nt, halves = 0;
+  if (!a.experts && full % 256 != 0 && full % 256 <= 128 && full > 256) {
+    halves = full % 256;
+    full -= halves;
+  }
+  const uint32_t blocks = (uint32_t)((halves ? full : (full + 7) / 8 * 8) + 2 * halves);
+  if (!halves) full = blocks;
+  q8_big_kernel<GATED><<<dim3(blocks), dim3(512), 0, st>>>(a, (int32_t)nt, (int32_t)mt, (int32_t)full);
+  return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
+}
 
 }  // namespace
 
 namespace vqi {
 
+size_t q8_one_lds(const OneArgs& a) {
+  const size_t slots = a.join ? a.slots : 1;
+  return slots * ((size_t)q8_row_bytes(a.k) + 8 * 64 * 16 * (a.join ? 1 : 2));
+}
+
+namespace {
+template <int RT, int WN, bool GATED, bool JOIN>
+vq_status launch_one_t(const OneArgs& a, hipStream_t st) {
+  const int out = WN * (GATED ? 16 : 16 * RT);
+  const dim3 g((uint32_t)((a.n + out - 1) / out), GATED ? a.slots : 1);
+  const size_t lds = (a.join ? a.slots : 1) * ((size_t)q8_row_bytes(a.k) + (size_t)8 * 64 * 16 * RT);
+  if (!grid_ok(g.x, 512)) return VQ_ERR_SHAPE;
+  if constexpr (JOIN) {  // the hidden rows are fp32
+    q8_one_kernel<RT, WN, GATED, JOIN, VQ_F32><<<g, dim3(512), lds, st>>>(a);
+  } else if (a.x_dtype == VQ_F32) {
+    q8_one_kernel<RT, WN, GATED, JOIN, VQ_F32><<<g, dim3(512), lds, st>>>(a);
+  } else if (a.x_dtype == VQ_F16) {
+    q8_one_kernel<RT, WN, GATED, JOIN, VQ_F16><<<g, dim3(512), lds, st>>>(a);
+  } else {
+    q8_one_kernel<RT, WN, GATED, JOIN, VQ_BF16><<<g, dim3(512), lds, st>>>(a);
+  }
+  return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
+}
+}  // namespace
+
+vq_status launch_q8_one(const OneArgs& a, void* stream) {
+  hipStream_t st = (hipStream_t)stream;
+  if (a.gated) return launch_one_t<2, 1, true, false>(a, st);
+  if (a.join) return launch_one_t<1, 1, false, true>(a, st);
+  switch (rows_per_group(a.n)) {
+    case 64: return launch_one_t<2, 2, false, false>(a, st);
+    case 32: return launch_one_t<2, 1, false, false>(a, st);
+    default: return launch_one_t<1, 1, false, false>(a, st);
+  }
+}
+
+// Few rows: streamed (q8_few_kernel), or, where the tokens' own traffic would outweigh that (each 16 or 32 weight rows
+// read them again), in 64-row tiles with K cut over the CUs.  28672 x 8192, 16 rows: 62 us streamed, 54 us in tiles;
+// 8192 x 8192: 18.4 and 22.2 us with 16 rows, 25.9 and 24.5 us with 64.
+static bool streamed(int32_t m, int32_t n, int32_t k) { return m <= 64 && (int64_t)m * n * k <= 2000000000; }
+
+// K is cut so far that the tiles fill the CUs once, three (64 rows) or two (128 rows) workgroups on each, at 14 (8)
+// steps of 128 or more per workgroup; not where a row of tiles nearly fills them, since the int32 partial sums are
+// written and read again.  128 x 8192 x 28672: 193 us uncut, 72 us in 4, 68 us in 8; 128 x 28672 x 8192: 69 us uncut,
+// 76 us in 2.
 int32_t q8_splits(int32_t m, int32_t n, int32_t k) {
-  if (m <= kFewRows) return 1;
-  const int64_t tiles = (((int64_t)m + 127) / 128) * (((int64_t)n + 127) / 128);
-  if (tiles >= 256) return 1;
-  const int64_t steps = q8_row_bytes(k) / kStep;
-  int64_t s = 512 / tiles;
-  if (s > steps / 8) s = steps / 8;
-  return s < 1 ? 1 : (int32_t)s;
+  if (streamed(m, n, k)) return 1;
+  const int64_t steps = q8_row_bytes(k) / kStep, nt = ((int64_t)n + 127) / 128;
+  if (m <= 64) return (int32_t)std::max<int64_t>(1, std::min<int64_t>(768 / nt, steps / 14));
+  const int64_t tiles = ((int64_t)m + 127) / 128 * nt;
+  return tiles >= 192 ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 8));
 }
 
 vq_status launch_q8(const Q8Args& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  const int64_t groups = a.experts ? (a.m < a.experts ? a.m : a.experts) : 1;
-  const int64_t avg = (a.m + groups - 1) / groups;
-  if (avg <= kFewRows) {
+  if (a.experts) {
+    // rows of a group on average (in the larger of max_rows' bound): short groups take small tiles.  Gated and plain
+    // product in us, 64 experts of 2048 x 1024, 4 of them for a token, with 32-, 64-, 128- and 256-row tiles:
+    //   333 tokens 54 + 29, 54 + 33, 63 + 36, 67 + 42;  2000 tokens 112 + 59, 100 + 57, 99 + 64, 109 + 85
+    // 8 experts of 4096 x 14336, 2 for a token: 1000 tokens 617 + 346, 508 + 291, 433 + 242, 414 + 197
+    const int64_t groups = a.m < a.experts ? a.m : a.experts;
+    const int64_t avg = (a.m + groups - 1) / groups;
     if (a.gated) {
-      if (avg <= 16) return launch_few<2, 1, true>(a, st);
-      if (avg <= 32) return launch_few<2, 2, true>(a, st);
-      return launch_few<2, 4, true>(a, st);
+      if (avg <= 4) return launch_tile<32, 128, 1, 2, true, false>(a, st);
+      if (avg <= 96) return launch_tile<64, 128, 2, 2, true, false>(a, st);
+      return avg <= 192 ? launch_tile<128, 128, 2, 2, true, false>(a, st) : launch_big<true>(a, st);
     }
-    if (avg <= 16) return launch_few<1, 1, false>(a, st);
-    if (avg <= 32) return launch_few<1, 2, false>(a, st);
-    return launch_few<1, 4, false>(a, st);
+    if (avg <= 48) return launch_tile<32, 128, 1, 4, false, false>(a, st);
+    return avg <= 192 ? launch_tile<128, 128, 2, 2, false, false>(a, st) : launch_big<false>(a, st);
   }
-  if (a.gated) return launch_tile<128, 128, 2, 2, true, false>(a, st);
+  if (streamed(a.m, a.n, a.k)) {
+    if (a.m <= 16) return launch_few_rows<1>(a, st);
+    if (a.m <= 32) return launch_few_rows<2>(a, st);
+    return a.m <= 48 ? launch_few_rows<3>(a, st) : launch_few_rows<4>(a, st);
+  }
   if (a.splits > 1) {
-    const vq_status e = launch_tile<128, 128, 2, 2, false, true>(a, st);
-    if (e != VQ_OK) return e;
-    const int64_t items = (int64_t)a.m * ((a.n + 3) / 4);  // under 256 tiles of 128 x 128: a small grid
-    q8_join_kernel<<<dim3((uint32_t)((items + 255) / 256)), dim3(256), 0, st>>>(a);
-    return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
+    const vq_status e = a.m <= 64 ? launch_tile<64, 128, 2, 2, false, true>(a, st)
+                                   : launch_tile<128, 128, 2, 2, false, true>(a, st);
+    return e != VQ_OK ? e : launch_join(a, st);
   }
-  return launch_tile<128, 128, 2, 2, false, false>(a, st);
+  if (a.m <= 64) return launch_tile<64, 128, 2, 2, false, false>(a, st);
+  const int64_t tiles = ((int64_t)a.m + 255) / 256 * (((int64_t)a.n + 255) / 256);
+  return tiles >= 256 ? launch_big<false>(a, st) : launch_tile<128, 128, 2, 2, false, false>(a, st);
 }
 
 }  // namespace vqi

@@ -172,6 +172,21 @@ vq_status vq_q8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype 
     return VQ_ERR_ALIGN;
   const LinearWs ws = linear_ws(M, N, K, workspace);
   if (workspace_bytes < ws.bytes) return VQ_ERR_BUFFER_SIZE;
+  if (M == 1) {  // the kernel cuts the token itself
+    OneArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.n = N;
+    a.k = K;
+    a.slots = 1;
+    a.x = x;
+    a.x_dtype = x_dtype;
+    a.w = (const uint8_t*)w;
+    a.sw = sw;
+    a.bias = (const uint16_t*)bias;
+    a.y = y;
+    a.y_dtype = y_dtype;
+    if (q8_one_lds(a) <= kQ8OneLds) return launch_q8_one(a, stream);
+  }
   const vq_status st = quantize(M, K, x, x_dtype, ldx, ws.q, ws.s, stream);
   if (st != VQ_OK) return st;
   return vq_q8_gemm(M, N, K, ws.q, ws.s, w, sw, bias, y, y_dtype, ws.splits > 1 ? ws.part : nullptr,
@@ -259,6 +274,37 @@ vq_status vq_q8_experts(int32_t tokens, int32_t top, int32_t experts, int32_t D,
   const ExpertsWs ws = experts_ws(tokens, top, experts, D, I, workspace);
   if (workspace_bytes < ws.bytes) return VQ_ERR_BUFFER_SIZE;
   const int32_t pairs = tokens * top;
+  if (tokens == 1 && top <= kQ8OneSlots) {  // no routing to sort: two launches
+    OneArgs in, out;
+    std::memset(&in, 0, sizeof in);
+    in.slots = top;
+    in.experts = experts;
+    in.ids = ids;
+    in.p = p;
+    out = in;
+    in.n = I;
+    in.k = D;
+    in.x = x;
+    in.x_dtype = x_dtype;
+    in.w = (const uint8_t*)w_in;
+    in.sw = s_in;
+    in.gated = 1;
+    in.y = ws.h;
+    in.y_dtype = VQ_F32;
+    out.n = D;
+    out.k = I;
+    out.x = ws.h;
+    out.x_dtype = VQ_F32;
+    out.w = (const uint8_t*)w_out;
+    out.sw = s_out;
+    out.join = 1;
+    out.y = y;
+    out.y_dtype = y_dtype;
+    if (q8_one_lds(in) <= kQ8OneLds && q8_one_lds(out) <= kQ8OneLds) {
+      if ((st = launch_q8_one(in, stream)) != VQ_OK) return st;
+      return launch_q8_one(out, stream);
+    }
+  }
   if ((st = launch_expert_plan(tokens, top, experts, ids, ws.offsets, ws.rows, ws.pos, stream)) != VQ_OK) return st;
   if ((st = quantize(tokens, D, x, x_dtype, ldx, ws.xq, ws.xs, stream)) != VQ_OK) return st;
   if ((st = vq_q8_gemm_grouped(experts, pairs, tokens, I, D, ws.offsets, ws.rows, ws.xq, ws.xs, w_in, s_in, nullptr, 1,

@@ -72,8 +72,14 @@ def _code(dt):
 
 
 def _stream(dev):
-    """Handle of the current stream of device index dev."""
-    return _torch().cuda.current_stream(dev).cuda_stream
+    """Handle of the current stream of device index dev (torch.cuda.current_stream(dev).cuda_stream, without its object)."""
+    return _torch()._C._cuda_getCurrentRawStream(dev)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_desc(*fields):
+    """A vq_norm_desc, by reference (it is only read)."""
+    return ctypes.byref(NormDesc(*fields))
 
 
 def _device(t, what):
@@ -329,10 +335,10 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
     else:
         x = z.new_empty((m, d), dtype=x_dtype or z.dtype)
         x_p, x_code = x.data_ptr(), _code(x.dtype)
-    desc = NormDesc(m, d, _KINDS[post], _KINDS[pre], z_code, h_code, VQ_F32 if w_dtype is None else _code(w_dtype),
-                    gate_code, x_code, min(int(gate_rows), 2 ** 31 - 1), eps, weight_offset, res_scale, gate_scale, ldz,
-                    ldh)
-    _check(lib().vq_block_norm(ctypes.byref(desc), zp, hp, *vecs, gate_p, r_p, x_p, q_p, s_p, _stream(dev)),
+    desc = _norm_desc(m, d, _KINDS[post], _KINDS[pre], z_code, h_code, VQ_F32 if w_dtype is None else _code(w_dtype),
+                      gate_code, x_code, min(int(gate_rows), 2 ** 31 - 1), eps, weight_offset, res_scale, gate_scale, ldz,
+                      ldh)
+    _check(lib().vq_block_norm(desc, zp, hp, *vecs, gate_p, r_p, x_p, q_p, s_p, _stream(dev)),
            "vq_block_norm")
     return (r, q, s) if q8 else (r, x)
 
