@@ -62,6 +62,18 @@ __device__ __forceinline__ bool find_span(const Q8Args& a, int32_t mt, Span& sp)
   }
   return false;
 }
+// Row tiles of the grouped product, as find_span counts them.
+template <int BM>
+__device__ __forceinline__ int32_t count_spans(const Q8Args& a) {
+  int32_t tiles = 0;
+  for (int32_t e = threadIdx.x & 63; e < a.experts; e += 64) {
+    const int32_t lo = min(max(a.offsets[e], 0), a.m), hi = min(max(a.offsets[e + 1], lo), a.m);
+    tiles += (hi - lo + BM - 1) / BM;
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) tiles += __shfl_xor(tiles, o, 64);
+  return __builtin_amdgcn_readfirstlane(tiles);
+}
 // Upper bound of the row tiles of a grouped product (sum of ceil(rows_e / bm)).
 inline int64_t span_bound(const Q8Args& a, int bm) {
   const int64_t e = a.m < a.experts ? a.m : a.experts;
@@ -226,30 +238,39 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
   if (kt0 + 1 < kt1) fetch(1);
   read(0, 0, 0);
   int buf = 0;
-  for (int32_t kt = kt0; kt < kt1; ++kt) {
-    read(1, buf, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(0);
-    __builtin_amdgcn_sched_barrier(0);
-    read(0, buf, 2);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(1);
-    __builtin_amdgcn_sched_barrier(0);
-    read(1, buf, 3);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(0);
-    __builtin_amdgcn_sched_barrier(0);
-    if (kt + 1 < kt1) {
-      __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): its part of the next step is in LDS, its last reads are done
-      __syncthreads();                     // and everyone's: the next step may be read, this one overwritten
-      if (kt + 2 < kt1) fetch(buf);
-      read(0, buf ^ 1, 0);
-      __builtin_amdgcn_sched_barrier(0);
+  auto mix = [&] {  // the reads of the next slice between the products of this one
+#pragma unroll
+    for (int i = 0; i < MI + NI; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
-    multiply(1);
+    __builtin_amdgcn_sched_group_barrier(0x008, MI * NI, 0);
     __builtin_amdgcn_sched_barrier(0);
+  };
+  auto first3 = [&] {
+    multiply(0);
+    read(1, buf, 1);
+    mix();
+    multiply(1);
+    read(0, buf, 2);
+    mix();
+    multiply(0);
+    read(1, buf, 3);
+    mix();
+  };
+  for (int32_t kt = kt0; kt + 1 < kt1; ++kt) {
+    first3();
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): its part of the next step is in LDS, its last reads are done
+    __syncthreads();                     // and everyone's: the next step may be read, this one overwritten
+    if (kt + 2 < kt1) fetch(buf);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1);
+    read(0, buf ^ 1, 0);
+    mix();
     buf ^= 1;
   }
+  first3();
+  multiply(1);
 
   // outputs: lane = token row0 + .., 16 consecutive channels per block
 #pragma unroll
@@ -314,15 +335,19 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
   }
 }
 
-// Tiles of one XCD (workgroup mod 8) are neighbours: 8 row tiles by all columns, columns slowest.  false: no such tile.
-__device__ __forceinline__ bool place(int32_t id, int32_t total, int32_t mt_count, int32_t nt, int32_t& mt, int32_t& nti) {
-  const int32_t per = (total + 7) / 8;
-  const int32_t at = (id & 7) * per + (id >> 3);
-  if ((id >> 3) >= per || at >= total) return false;
+// Order of the tiles: 8 row tiles by all columns, columns slowest.
+__device__ __forceinline__ void tile_at(int32_t at, int32_t mt_count, int32_t nt, int32_t& mt, int32_t& nti) {
   const int32_t band = at / (8 * nt), in_band = at - band * 8 * nt;
   const int32_t band_rows = min(8, mt_count - band * 8);
   mt = band * 8 + in_band % band_rows;
   nti = in_band / band_rows;
+}
+// The tile of workgroup `id`: those of one XCD (id mod 8) are neighbours in that order.  false: no such tile.
+__device__ __forceinline__ bool place(int32_t id, int32_t total, int32_t mt_count, int32_t nt, int32_t& mt, int32_t& nti) {
+  const int32_t per = (total + 7) / 8;
+  const int32_t at = (id & 7) * per + (id >> 3);
+  if ((id >> 3) >= per || at >= total) return false;
+  tile_at(at, mt_count, nt, mt, nti);
   return true;
 }
 
@@ -337,26 +362,28 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t
   tile<BM, BN, WM, WN, GATED, SPLIT>(a, sp, nti * (GATED ? BN / 2 : BN), lds);
 }
 
-// 256 x 256 tiles on 8 wavefronts, one workgroup per CU: half the LDS reads and a third fewer matrix bytes per operation
-// than 128 x 128.  Tiles of 128 rows where a group's (or the matrix's) last tile has no more left, and for the tiles from
-// `full` on, which are the last, partial round over the CUs: two half tiles there take one round of half the length.
+// 256 x 256 tiles on 8 wavefronts, one workgroup per CU: half the LDS reads and half the matrix bytes per operation of
+// 128 x 128.  128 rows only where a group's (or the matrix's) last tile has no more left, and in the last round over the
+// 256 CUs if at most half of them have a tile in it: two half tiles for each then take half a round.
+// 4096 x 14336 x 4096 (3.5 rounds): 241 us with whole tiles only, 224 us.
 template <bool GATED>
-__global__ __launch_bounds__(512) void q8_big_kernel(Q8Args a, int32_t nt, int32_t mt_count, int32_t full) {
+__global__ __launch_bounds__(512) void q8_big_kernel(Q8Args a, int32_t nt, int32_t mt_count) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * 512 * kStep];
-  const int32_t out = GATED ? 128 : 256;
-  int32_t mt, nti, part = 0;
+  if (a.experts) mt_count = count_spans<256>(a);  // the launch has room for the bound
+  const int32_t total = mt_count * nt;
+  const int32_t rest = total % 256;
+  const int32_t full = rest <= 128 ? total - rest : total;  // ids from the next multiple of 8 on are halves
+  const int32_t whole = (full + 7) / 8 * 8;
   const int32_t id = (int32_t)blockIdx.x;
-  const bool half = id >= full;
-  if (!half) {
-    if (!place(id, min(full, mt_count * nt), mt_count, nt, mt, nti)) return;
-  } else {
-    const int32_t at = full + (id - full) / 2;
-    if (at >= mt_count * nt) return;
-    part = (id - full) & 1;
-    const int32_t band = at / (8 * nt), in_band = at - band * 8 * nt;
-    const int32_t band_rows = min(8, mt_count - band * 8);
-    mt = band * 8 + in_band % band_rows;
-    nti = in_band / band_rows;
+  int32_t mt, nti, part = 0;
+  const bool half = id >= whole;
+  if (half) {
+    const int32_t at = full + (id - whole) / 2;
+    if (at >= total) return;
+    part = (id - whole) & 1;
+    tile_at(at, mt_count, nt, mt, nti);
+  } else if (!place(id, full, mt_count, nt, mt, nti)) {
+    return;
   }
   Span sp{0, mt * 256, a.m};
   if (a.experts && !find_span<256>(a, mt, sp)) return;
@@ -364,9 +391,9 @@ __global__ __launch_bounds__(512) void q8_big_kernel(Q8Args a, int32_t nt, int32
   if (sp.row0 >= sp.end) return;
   if (half) sp.end = min(sp.end, sp.row0 + 128);
   if (half || sp.end - sp.row0 <= 128) {
-    tile<128, 256, 2, 4, GATED, false>(a, sp, nti * out, lds);
+    tile<128, 256, 2, 4, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
   } else {
-    tile<256, 256, 2, 4, GATED, false>(a, sp, nti * out, lds);
+    tile<256, 256, 2, 4, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
   }
 }
 
@@ -777,17 +804,9 @@ vq_status launch_big(const Q8Args& a, hipStream_t st) {
   const int out = GATED ? 128 : 256;
   const int64_t mt = a.experts ? span_bound(a, 256) : ((int64_t)a.m + 255) / 256;
   const int64_t nt = ((int64_t)a.n + out - 1) / out;
-  if (!vqi::grid_ok(2 * mt * nt + 8, 512)) return VQ_ERR_SHAPE;
-  // whole rounds of 256 tiles, then the rest in halves where they fit one round; a grouped product's tiles are a bound,
-  // so its last round is not known here
-  int64_t full = mt * nt, halves = 0;
-  if (!a.experts && full % 256 != 0 && full % 256 <= 128 && full > 256) {
-    halves = full % 256;
-    full -= halves;
-  }
-  const uint32_t blocks = (uint32_t)((halves ? full : (full + 7) / 8 * 8) + 2 * halves);
-  if (!halves) full = blocks;
-  q8_big_kernel<GATED><<<dim3(blocks), dim3(512), 0, st>>>(a, (int32_t)nt, (int32_t)mt, (int32_t)full);
+  const int64_t blocks = mt * nt + 128 + 8;  // at most 128 tiles are cut in two
+  if (!vqi::grid_ok(blocks, 512)) return VQ_ERR_SHAPE;
+  q8_big_kernel<GATED><<<dim3((uint32_t)blocks), dim3(512), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
 }
 
