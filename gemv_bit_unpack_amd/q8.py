@@ -128,6 +128,13 @@ def _ws(ws, dev):
     return (None, 0) if ws is None else (_ptr(ws, "workspace", None, dev), ws.numel() * ws.element_size())
 
 
+def _like(t, dtype):
+    """A new tensor of t's shape, contiguous."""
+    if t.dtype is dtype and t.is_contiguous():
+        return _torch().empty_like(t)
+    return t.new_empty(t.shape, dtype=dtype)
+
+
 def _out(out, shape, dtype, like):
     """An output of this shape: `out` itself, checked by _ptr later, or a new tensor on like's device."""
     return like.new_empty(shape, dtype=dtype) if out is None else out
@@ -294,8 +301,8 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
     [ceil(M / gate_rows), D] with one row for every gate_rows rows.  Returns (r, x), or with ``q8`` (r, q, s): x in
     8 bits.  r has the residual's dtype (z's without one); ``r_out`` may be the residual itself; ``keep_r=False``
     returns None for it.  x_dtype defaults to z's."""
-    torch = _torch()
-    if post not in _KINDS or pre not in _KINDS:
+    kinds = _KINDS.get(post), _KINDS.get(pre)
+    if None in kinds:
         raise ValueError("post and pre must be one of %s" % (tuple(_KINDS),))
     zp, ldz, z_code, dev = _rows(z, "z")
     m, d = z.shape
@@ -307,13 +314,14 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
         if h_dev != dev:
             raise ValueError("residual must be on device %d, is on %s" % (dev, residual.device))
         r_dtype = residual.dtype
-    w_dtype, vecs = None, []
-    for v in (post_weight, post_bias, pre_weight, pre_bias):
+    w_dtype, vecs = None, [None] * 4
+    for i, v in enumerate((post_weight, post_bias, pre_weight, pre_bias)):
         if v is not None:
-            w_dtype = w_dtype or v.dtype
-            if v.dtype is not w_dtype:
+            if w_dtype is None:
+                w_dtype = v.dtype
+            elif v.dtype is not w_dtype:
                 raise TypeError("norm weights and biases must share one dtype")
-        vecs.append(_ptr(v, "a norm weight or bias", (d,), dev))
+            vecs[i] = _ptr(v, "a norm weight or bias", (d,), dev)
     gate_p, gate_code = None, VQ_F32
     if gate is not None:
         if gate.dim() == 1:
@@ -323,23 +331,24 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
         else:
             shape = (-(-m // gate_rows), d)
         gate_p, gate_code = _ptr(gate, "gate", shape, dev), _code(gate.dtype)
-    r = r_p = None
-    if keep_r or r_out is not None:
-        r = _out(r_out, (m, d), r_dtype, z)
-        r_p = _ptr(r, "r_out", (m, d), dev, r_dtype)
+    r, r_p = r_out, None
+    if r_out is not None:
+        r_p = _ptr(r_out, "r_out", (m, d), dev, r_dtype)
+    elif keep_r:
+        r = _like(z if residual is None else residual, r_dtype)
+        r_p = r.data_ptr()
     x = q = s = x_p = q_p = s_p = None
     x_code = VQ_F32
     if q8:
+        torch = _torch()
         q, s = z.new_empty((m, q8_row_bytes(d)), dtype=torch.int8), z.new_empty((m,), dtype=torch.float32)
         q_p, s_p = q.data_ptr(), s.data_ptr()
     else:
-        x = z.new_empty((m, d), dtype=x_dtype or z.dtype)
+        x = _like(z, x_dtype or z.dtype)
         x_p, x_code = x.data_ptr(), _code(x.dtype)
-    desc = _norm_desc(m, d, _KINDS[post], _KINDS[pre], z_code, h_code, VQ_F32 if w_dtype is None else _code(w_dtype),
-                      gate_code, x_code, min(int(gate_rows), 2 ** 31 - 1), eps, weight_offset, res_scale, gate_scale, ldz,
-                      ldh)
-    _check(lib().vq_block_norm(desc, zp, hp, *vecs, gate_p, r_p, x_p, q_p, s_p, _stream(dev)),
-           "vq_block_norm")
+    desc = _norm_desc(m, d, *kinds, z_code, h_code, VQ_F32 if w_dtype is None else _code(w_dtype), gate_code, x_code,
+                      min(int(gate_rows), 2 ** 31 - 1), eps, weight_offset, res_scale, gate_scale, ldz, ldh)
+    _check(lib().vq_block_norm(desc, zp, hp, *vecs, gate_p, r_p, x_p, q_p, s_p, _stream(dev)), "vq_block_norm")
     return (r, q, s) if q8 else (r, x)
 
 

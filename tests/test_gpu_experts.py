@@ -114,6 +114,37 @@ def test_grouped_products(vq, t, e, top, d, i, how):
             q8ref.check(z[a:b], ref, bound, "f32")
 
 
+@pytest.mark.parametrize("gated", [True, False])
+def test_grouped_many_tiles(vq, gated):
+    """Groups long enough for 256-row tiles, and enough tiles for several rounds over the CUs, the last one in halves."""
+    g = np.random.default_rng(77)
+    t, e, top, d, n = 2500, 5, 2, 70, 4000
+    ids = _ids(g, t, e, top)
+    off, rows, pos = q8ref.plan(ids, e)
+    w = np.clip(np.rint(g.standard_normal((e, 2 * n, d)) * 40), -127, 127).astype(np.int8)
+    sw = g.uniform(0.5, 1.5, (e, 2 * n)).astype(np.float32) * np.float32(3e-3)
+    q, s = vq.q8_quantize(_x(g, t, d, "bf16"))
+    y = vq.q8_gemm_grouped(cu(off), cu(rows), q, s, vq.q8_pad(cu(w)), cu(sw), None, d, t * top, gated=gated)
+    qn, sn = q[:, :d].cpu().numpy(), s.cpu().numpy()
+    for ex in range(e):
+        a, b = off[ex], off[ex + 1]
+        ref, bound = (q8ref.gated if gated else q8ref.product)(qn[rows[a:b]], sn[rows[a:b]], w[ex], sw[ex])
+        q8ref.check(y[a:b], ref, bound, "f32")
+
+
+def test_groups_outside_the_buffer_are_bounded(vq):
+    """Offsets and rows that no plan wrote: nothing is read or written outside the buffers that were given."""
+    g = np.random.default_rng(5)
+    w_in, s_in, _, _ = _layer(g, 3, 64, 32)
+    q, s = vq.q8_quantize(_x(g, 6, 64, "f32"))
+    for off, rows in (([-5, 2, 4, 1000], [0, 1, 2, 3, 4, 5]), ([3, 1, 6, 2], [9, -1, 5, 70000, 0, 2])):
+        guard = torch.full((10, 32), 7.0, device="cuda")
+        vq.q8_gemm_grouped(cu(np.array(off, np.int32)), cu(np.array(rows, np.int32)), q, s, vq.q8_pad(cu(w_in)),
+                           cu(s_in), None, 64, 6, gated=True, out=guard[2:8])
+        torch.cuda.synchronize()
+        assert bool((guard[:2] == 7.0).all()) and bool((guard[8:] == 7.0).all())
+
+
 @pytest.mark.parametrize("t,top,n", [(1, 1, 1), (3, 2, 5), (40, 4, 130), (300, 2, 1027), (2, 8, 4096)])
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
 def test_combine(vq, t, top, n, out):
@@ -147,6 +178,30 @@ def test_whole_layer_equals_its_parts(vq, t, e, top, d, i, how, dt):
     z = vq.q8_gemm_grouped(off, None, hq, hs, lay.w_out, s_out, None, i, r, out=torch.zeros((r, d), device="cuda"))
     want = vq.expert_combine(z, pos, p, y_dtype=DT[dt])
     assert y.dtype == x.dtype and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("e,top,d,i", [(8, 2, 256, 384), (4, 4, 1000, 333), (12, 9, 128, 100), (6, 2, 130, 40000),
+                                       (6, 2, 40000, 130), (2, 1, 1, 1)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_one_token_layer(vq, e, top, d, i, dt):
+    """One token: its own two launches, and more slots or longer rows than those take; ids of no expert among them."""
+    g = np.random.default_rng([e, top, d, i])
+    w_in, s_in, w_out, s_out = (cu(v) for v in _layer(g, e, d, i))
+    lay = vq.Q8Experts(w_in, s_in, w_out, s_out)
+    x, p = _x(g, 1, d, dt), cu(g.random((1, top)).astype(np.float32))
+    full = _ids(g, 1, e, top)
+    for drop in ((), (0,), tuple(range(top))):
+        ids = full.copy()
+        ids[0, list(drop)] = -1 if len(drop) == 1 else e
+        y = lay(x, cu(ids), p, y_dtype=torch.float32)
+        off, rows, pos = vq.expert_plan(cu(ids), e)
+        q, s = vq.q8_quantize(x)
+        h = vq.q8_gemm_grouped(off, rows, q, s, lay.w_in, s_in, None, d, top, gated=True,
+                               out=torch.zeros((top, i), device="cuda"))
+        hq, hs = vq.q8_quantize(h)
+        z = vq.q8_gemm_grouped(off, None, hq, hs, lay.w_out, s_out, None, i, top, out=torch.zeros((top, d), device="cuda"))
+        assert torch.equal(y, vq.expert_combine(z, pos, p)), drop
+    assert not y.any()
 
 
 def test_whole_layer_against_dense(vq):

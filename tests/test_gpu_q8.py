@@ -117,6 +117,42 @@ def test_gemm(vq, m, n, k, out, bias):
     assert torch.equal(y, vq.q8_linear(x, *args[2:5], lw, y_dtype=DT[out]))
 
 
+@pytest.mark.parametrize("m,n,k", [(4200, 4100, 130), (5000, 4999, 100)])
+def test_gemm_many_tiles(vq, m, n, k):
+    """Enough 256 x 256 tiles to fill the CUs: 289 of them (33 in the second round, cut in halves) and 400."""
+    g = np.random.default_rng([m, n, k])
+    x = _x(g, m, k, "bf16")
+    w, sw = _w(g, n, k)
+    q, s = vq.q8_quantize(x)
+    y = vq.q8_gemm(q, s, _q(vq, w), torch.from_numpy(sw).cuda(), None, k, y_dtype=torch.float32)
+    ref, bound = q8ref.product(q[:, :k].cpu().numpy(), s.cpu().numpy(), w, sw)
+    q8ref.check(y, ref, bound, "f32")
+
+
+@pytest.mark.parametrize("n,k", [(1, 1), (70, 57345), (3, 60000), (5000, 129), (13000, 333), (256, 14336)])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_one_token(vq, n, k, dt):
+    """The form that cuts its token inside the product, and rows too long for it: the same bits as the two steps."""
+    g = np.random.default_rng([n, k])
+    x = _x(g, 1, k, dt)
+    w, sw = _w(g, n, k)
+    b = (g.standard_normal(n) * 0.3).astype(np.float16)
+    wd, swd, bd = _q(vq, w), torch.from_numpy(sw).cuda(), torch.from_numpy(b).cuda()
+    ws = torch.empty(vq.q8_linear_workspace_bytes(1, n, k), dtype=torch.uint8, device="cuda")
+    y = vq.q8_linear(x, wd, swd, bd, ws, y_dtype=torch.float32)
+    q, s = q8ref.quantize(q8ref.widen(x))
+    ref, bound = q8ref.product(q, s, w, sw, b)
+    q8ref.check(y, ref, bound, "f32")
+    q2, s2 = vq.q8_quantize(x)
+    assert torch.equal(y, vq.q8_gemm(q2, s2, wd, swd, bd, k, y_dtype=torch.float32))
+    for bad in (float("nan"), float("inf")):
+        x2 = x.clone()
+        x2[0, k // 2] = bad
+        assert bool(torch.isnan(vq.q8_linear(x2, wd, swd, bd, ws)).all())
+    zero = vq.q8_linear(torch.zeros_like(x), wd, swd, bd, ws, y_dtype=torch.float32)
+    assert torch.equal(zero[0], bd.float())
+
+
 def test_gemm_extreme_integers(vq):
     """All products at their largest: K = 65536 sums of 127 * -128 stay exact."""
     for m in (1, 16, 80):
