@@ -141,16 +141,31 @@ __device__ __forceinline__ void to_lds(const uint8_t* g, uint8_t* l) {
                                    (__attribute__((address_space(3))) void*)l, 16, 0, 0);
 }
 
+// The workgroup's barrier alone.  __syncthreads() would also wait for every load to LDS that is still on its way; here
+// each wavefront has waited for those that the others need, and for its own reads, and no memory operation moves across.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
 // One tile: WM x WN wavefronts compute BM rows (from row0, those below end) by BN weight rows (with the gate: BN / 2
 // outputs, 32-row blocks of gate and up rows in turn, so that a lane ends with both values of an output).  The weights
 // are the matrix instruction's first operand: a lane then holds 16 outputs of one token, and since block row i holds
 // weight row perm(i) they are 16 consecutive ones.
-template <int BM, int BN, int WM, int WN, bool GATED, bool SPLIT>
+template <int BM, int BN, int WM, int WN, int NB, bool GATED, bool SPLIT>
 __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0, uint8_t* lds) {
   constexpr int kWaves = WM * WN;
   constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
   constexpr int TL = BM / 8 / kWaves, WL = BN / 8 / kWaves;  // 8-row loads per wavefront and step
   constexpr int kBuf = (BM + BN) * kStep;
+  // steps in LDS: one is read while NB - 1 are on their way; vmcnt of a wavefront whose loads of one step more than the
+  // next may be outstanding
+  constexpr int kLater = (NB - 2) * (TL + WL);
+  static_assert(NB >= 2 && kLater < 64, "the wait counter holds 6 bits");
+  constexpr int kWaitNext = 0x0070 | (kLater & 15) | (kLater >> 4) << 14;  // and lgkmcnt(0)
   static_assert(TL * 8 * kWaves == BM && WL * 8 * kWaves == BN, "whole loads");
   static_assert(!GATED || NI % 2 == 0, "gate and up blocks in one wavefront");
 
@@ -232,10 +247,16 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][j], ft[set][i], acc[i][j], 0, 0, 0);
   };
 
-  fetch(0);
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wavefront's part of the first step is in LDS
-  __syncthreads();                     // and everyone's
-  if (kt0 + 1 < kt1) fetch(1);
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+    if (b < NB - 1 && kt0 + b < kt1) fetch(b);
+  if (kt0 + NB - 1 <= kt1) {
+    __builtin_amdgcn_s_waitcnt(kWaitNext);  // this wavefront's part of the first step is in LDS
+  } else {
+    __builtin_amdgcn_s_waitcnt(0x0070);
+  }
+  meet();  // and everyone's
+  if (kt0 + NB - 1 < kt1) fetch(NB - 1);
   read(0, 0, 0);
   int buf = 0;
   auto mix = [&] {  // the reads of the next slice between the products of this one
@@ -260,14 +281,20 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
   };
   for (int32_t kt = kt0; kt + 1 < kt1; ++kt) {
     first3();
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): its part of the next step is in LDS, its last reads are done
-    __syncthreads();                     // and everyone's: the next step may be read, this one overwritten
-    if (kt + 2 < kt1) fetch(buf);
+    // its part of the next step is in LDS (steps after that may still be on their way), its last reads are done
+    if (kt + NB - 1 < kt1) {
+      __builtin_amdgcn_s_waitcnt(kWaitNext);
+    } else {
+      __builtin_amdgcn_s_waitcnt(0x0070);
+    }
+    meet();  // and everyone's: the next step may be read, this one overwritten
+    if (kt + NB < kt1) fetch(buf);
+    const int next = buf + 1 == NB ? 0 : buf + 1;
     __builtin_amdgcn_sched_barrier(0);
     multiply(1);
-    read(0, buf ^ 1, 0);
+    read(0, next, 0);
     mix();
-    buf ^= 1;
+    buf = next;
   }
   first3();
   multiply(1);
@@ -352,14 +379,14 @@ __device__ __forceinline__ bool place(int32_t id, int32_t total, int32_t mt_coun
 }
 
 // Tiles with several workgroups per CU.
-template <int BM, int BN, int WM, int WN, bool GATED, bool SPLIT>
+template <int BM, int BN, int WM, int WN, int NB, bool GATED, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t nt, int32_t mt_count) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (BM + BN) * kStep];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NB * (BM + BN) * kStep];
   int32_t mt, nti;
   if (!place((int32_t)blockIdx.x, mt_count * nt, mt_count, nt, mt, nti)) return;
   Span sp{0, mt * BM, a.m};
   if (a.experts && !find_span<BM>(a, mt, sp)) return;
-  tile<BM, BN, WM, WN, GATED, SPLIT>(a, sp, nti * (GATED ? BN / 2 : BN), lds);
+  tile<BM, BN, WM, WN, NB, GATED, SPLIT>(a, sp, nti * (GATED ? BN / 2 : BN), lds);
 }
 
 // 256 x 256 tiles on 8 wavefronts, one workgroup per CU: half the LDS reads and half the matrix bytes per operation of
@@ -391,9 +418,9 @@ __global__ __launch_bounds__(512) void q8_big_kernel(Q8Args a, int32_t nt, int32
   if (sp.row0 >= sp.end) return;
   if (half) sp.end = min(sp.end, sp.row0 + 128);
   if (half || sp.end - sp.row0 <= 128) {
-    tile<128, 256, 2, 4, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
+    tile<128, 256, 2, 4, 2, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
   } else {
-    tile<256, 256, 2, 4, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
+    tile<256, 256, 2, 4, 2, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
   }
 }
 
@@ -783,19 +810,19 @@ vq_status launch_few_rows(const Q8Args& a, hipStream_t st) {
   }
 }
 
-template <int BM, int BN, int WM, int WN, bool GATED, bool SPLIT>
+template <int BM, int BN, int WM, int WN, int NB, bool GATED, bool SPLIT>
 vq_status launch_tile(const Q8Args& a, hipStream_t st) {
   const int out = GATED ? BN / 2 : BN;
   const int64_t mt = a.experts ? span_bound(a, BM) : ((int64_t)a.m + BM - 1) / BM;
   const int64_t nt = ((int64_t)a.n + out - 1) / out;
   if (!vqi::grid_ok(mt * nt + 8, 64 * WM * WN)) return VQ_ERR_SHAPE;
   const uint32_t blocks = (uint32_t)((mt * nt + 7) / 8 * 8);
-  q8_tile_kernel<BM, BN, WM, WN, GATED, SPLIT>
+  q8_tile_kernel<BM, BN, WM, WN, NB, GATED, SPLIT>
       <<<dim3(blocks, SPLIT ? a.splits : 1), dim3(64 * WM * WN), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
 }
 vq_status launch_join(const Q8Args& a, hipStream_t st) {
-  const int64_t items = (int64_t)a.m * ((a.n + 3) / 4);  // under 256 tiles of 128 x 128: a small grid
+  const int64_t items = (int64_t)a.m * ((a.n + 3) / 4);  // at most 128 tiles of 128 x 128: a small grid
   q8_join_kernel<<<dim3((uint32_t)((items + 255) / 256)), dim3(256), 0, st>>>(a);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
 }
@@ -850,22 +877,41 @@ vq_status launch_q8_one(const OneArgs& a, void* stream) {
   }
 }
 
-// Few rows: streamed (q8_few_kernel), or, where the tokens' own traffic would outweigh that (each 16 or 32 weight rows
-// read them again), in 64-row tiles with K cut over the CUs.  28672 x 8192, 16 rows: 62 us streamed, 54 us in tiles;
-// 8192 x 8192: 18.4 and 22.2 us with 16 rows, 25.9 and 24.5 us with 64.
-static bool streamed(int32_t m, int32_t n, int32_t k) { return m <= 64 && (int64_t)m * n * k <= 2000000000; }
-
-// K is cut so far that the tiles fill the CUs once, three (64 rows) or two (128 rows) workgroups on each, at 14 (8)
-// steps of 128 or more per workgroup; not where a row of tiles nearly fills them, since the int32 partial sums are
-// written and read again.  128 x 8192 x 28672: 193 us uncut, 72 us in 4, 68 us in 8; 128 x 28672 x 8192: 69 us uncut,
-// 76 us in 2.
-int32_t q8_splits(int32_t m, int32_t n, int32_t k) {
-  if (streamed(m, n, k)) return 1;
-  const int64_t steps = q8_row_bytes(k) / kStep, nt = ((int64_t)n + 127) / 128;
-  if (m <= 64) return (int32_t)std::max<int64_t>(1, std::min<int64_t>(768 / nt, steps / 14));
-  const int64_t tiles = ((int64_t)m + 127) / 128 * nt;
-  return tiles >= 192 ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 8));
+// How a dense product is computed.  kStreamed: q8_few_kernel.  The tiles differ in rows x columns and in the steps kept
+// in LDS: one step of a tile takes about a microsecond to arrive, so a CU with one workgroup moves what the workgroup
+// has on its way in that time.
+namespace {
+enum Way { kStreamed, k64x64, k128x64, k128x128, k128x128Pair, k256x256 };
+struct Plan {
+  Way way;
+  int32_t splits;  // cuts of K over the CUs
+};
+Plan dense_plan(int32_t m, int32_t n, int32_t k) {
+  // us, rows x 5003 x 4099: 16 rows 11.2 streamed, 12.4 in 64 x 64; 48 rows 15.6 and 12.4.  14336 x 4096: 2 rows 16.5
+  // and 17.1, 32 rows 19.8 and 16.0
+  if (m <= 64 && (int64_t)m * n * k <= 600000000) return {kStreamed, 1};
+  const int64_t steps = q8_row_bytes(k) / kStep;
+  auto tiles = [&](int bm, int bn) { return (((int64_t)m + bm - 1) / bm) * (((int64_t)n + bn - 1) / bn); };
+  // K is cut where the tiles leave CUs without work, at 28 steps or more each: the int32 partial sums cost a second launch
+  auto cut = [&](int64_t t) { return (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / t, steps / 28)); };
+  const int64_t small = tiles(64, 64), tall = tiles(128, 64), wide = tiles(128, 128);
+  // 512 x 28672 x 8192 (224 of them): 117 us against 156 in 128 x 128; 1024 x 8192 x 8192 (128): 100 against 73
+  if (tiles(256, 256) >= 200) return {k256x256, 1};
+  // 64 x 28672 x 8192: 53 us; 128 x 4096 x 4096: 11.8 against 15.0 in 128 x 64 and 22 in 128 x 128; 64 x 4096 x 14336:
+  // 19.4 cut in 4, 37 uncut.  128 x 8192 x 28672, where each step counts: 82 us against 63 in 128 x 128 cut in 4
+  if (m <= 64 || (small <= 256 && steps < 100)) return {k64x64, cut(small)};
+  // 128 x 14336 x 4096: 20.8 us against 23.8 in 64 x 64 and 26.2 in 128 x 128; 256 x 8192 x 8192: 33.7, 41.4 and 37.8
+  if (tall >= 160 && tall <= 256 && steps < 128) return {k128x64, 1};
+  // 512 x 4096 x 4096: 17.0 us against 22.4 in 128 x 128
+  if (small <= 512 && steps < 40) return {k64x64, 1};
+  // one workgroup per CU and three steps in LDS, or two workgroups and two steps: 128 x 28672 x 8192 (224 tiles) 60.7
+  // and 71.6 us, 512 x 14336 x 4096 (448) 49.5 and 44.1
+  if (wide <= 256) return {k128x128, cut(wide)};
+  return {k128x128Pair, 1};
 }
+}  // namespace
+
+int32_t q8_splits(int32_t m, int32_t n, int32_t k) { return dense_plan(m, n, k).splits; }
 
 vq_status launch_q8(const Q8Args& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
@@ -877,26 +923,33 @@ vq_status launch_q8(const Q8Args& a, void* stream) {
     const int64_t groups = a.m < a.experts ? a.m : a.experts;
     const int64_t avg = (a.m + groups - 1) / groups;
     if (a.gated) {
-      if (avg <= 4) return launch_tile<32, 128, 1, 2, true, false>(a, st);
-      if (avg <= 96) return launch_tile<64, 128, 2, 2, true, false>(a, st);
-      return avg <= 192 ? launch_tile<128, 128, 2, 2, true, false>(a, st) : launch_big<true>(a, st);
+      if (avg <= 4) return launch_tile<32, 128, 1, 2, 2, true, false>(a, st);
+      if (avg <= 96) return launch_tile<64, 128, 2, 2, 2, true, false>(a, st);
+      return avg <= 192 ? launch_tile<128, 128, 2, 2, 2, true, false>(a, st) : launch_big<true>(a, st);
     }
-    if (avg <= 48) return launch_tile<32, 128, 1, 4, false, false>(a, st);
-    return avg <= 192 ? launch_tile<128, 128, 2, 2, false, false>(a, st) : launch_big<false>(a, st);
+    if (avg <= 48) return launch_tile<32, 128, 1, 4, 2, false, false>(a, st);
+    return avg <= 192 ? launch_tile<128, 128, 2, 2, 2, false, false>(a, st) : launch_big<false>(a, st);
   }
-  if (streamed(a.m, a.n, a.k)) {
-    if (a.m <= 16) return launch_few_rows<1>(a, st);
-    if (a.m <= 32) return launch_few_rows<2>(a, st);
-    return a.m <= 48 ? launch_few_rows<3>(a, st) : launch_few_rows<4>(a, st);
+  switch (dense_plan(a.m, a.n, a.k).way) {
+    case kStreamed:
+      if (a.m <= 16) return launch_few_rows<1>(a, st);
+      if (a.m <= 32) return launch_few_rows<2>(a, st);
+      return a.m <= 48 ? launch_few_rows<3>(a, st) : launch_few_rows<4>(a, st);
+    case k64x64: {
+      if (a.splits == 1) return launch_tile<64, 64, 2, 2, 4, false, false>(a, st);
+      const vq_status e = launch_tile<64, 64, 2, 2, 4, false, true>(a, st);
+      return e != VQ_OK ? e : launch_join(a, st);
+    }
+    case k128x64: return launch_tile<128, 64, 2, 2, 3, false, false>(a, st);
+    case k128x128: {
+      if (a.splits == 1) return launch_tile<128, 128, 2, 2, 3, false, false>(a, st);
+      const vq_status e = launch_tile<128, 128, 2, 2, 3, false, true>(a, st);
+      return e != VQ_OK ? e : launch_join(a, st);
+    }
+    case k128x128Pair: return launch_tile<128, 128, 2, 2, 2, false, false>(a, st);
+    case k256x256: return launch_big<false>(a, st);
   }
-  if (a.splits > 1) {
-    const vq_status e = a.m <= 64 ? launch_tile<64, 128, 2, 2, false, true>(a, st)
-                                   : launch_tile<128, 128, 2, 2, false, true>(a, st);
-    return e != VQ_OK ? e : launch_join(a, st);
-  }
-  if (a.m <= 64) return launch_tile<64, 128, 2, 2, false, false>(a, st);
-  const int64_t tiles = ((int64_t)a.m + 255) / 256 * (((int64_t)a.n + 255) / 256);
-  return tiles >= 256 ? launch_big<false>(a, st) : launch_tile<128, 128, 2, 2, false, false>(a, st);
+  return VQ_ERR_UNSUPPORTED;
 }
 
 }  // namespace vqi
