@@ -10,6 +10,7 @@ namespace {
 // threads gives every thread its first row, and the second sweep writes.  The pairs of an expert keep their order, so
 // the plan does not depend on timing.  The id list is read 2 E times, from the caches: 16384 pairs are 64 KiB.
 constexpr int kThreads = 1024;
+constexpr int kHeld = 8;
 
 __global__ __launch_bounds__(kThreads) void expert_plan_kernel(int32_t pairs, int32_t top, int32_t experts,
                                                               const int32_t* __restrict__ ids,
@@ -22,11 +23,16 @@ __global__ __launch_bounds__(kThreads) void expert_plan_kernel(int32_t pairs, in
   const int64_t first = (int64_t)t * share;
   const int32_t lo = (int32_t)min(first, (int64_t)pairs), hi = (int32_t)min(first + share, (int64_t)pairs);
   int32_t eq = 0, lt = 0;
-  for (int32_t i = lo; i < hi; ++i) {
-    const int32_t id = ids[i];
+  int32_t held[kHeld];  // the share's first ids, loaded together and kept for the second sweep
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) held[k] = lo + k < hi ? ids[lo + k] : -1;
+  auto count = [&](int32_t id) {
     eq += id == e;
     lt += id >= 0 && id < e;
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) count(held[k]);
+  for (int32_t i = lo + kHeld; i < hi; ++i) count(ids[i]);
   int32_t incl = eq;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -51,15 +57,18 @@ __global__ __launch_bounds__(kThreads) void expert_plan_kernel(int32_t pairs, in
     if (e == experts - 1) offsets[experts] = base + all;
   }
   int32_t at = base + below + incl - eq;
-  for (int32_t i = lo; i < hi; ++i) {
-    const int32_t id = ids[i];
+  auto place = [&](int32_t i, int32_t id) {
     if (id == e) {
       rows[at] = i / top;
       pos[i] = at++;
     } else if (e == 0 && (id < 0 || id >= experts)) {
       pos[i] = -1;  // no expert here: the pair is dropped
     }
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (lo + k < hi) place(lo + k, held[k]);
+  for (int32_t i = lo + kHeld; i < hi; ++i) place(i, ids[i]);
 }
 
 // y[t] = sum_j p[t][j] z[pos[t][j]] in fp32, j ascending; 4 columns per thread.
