@@ -50,13 +50,11 @@ __device__ __forceinline__ bool find_span(const Q8Args& a, int32_t mt, Span& sp)
     const uint64_t hit = __ballot(mt < before + incl);
     if (hit) {
       const int at = __builtin_ctzll(hit);
-      sp.e = e0 + at;
-      sp.row0 = __shfl(lo + (mt - before - (incl - tiles)) * BM, at, 64);
-      sp.end = __shfl(hi, at, 64);
-      sp.e = __builtin_amdgcn_readfirstlane(sp.e);
-      sp.row0 = __builtin_amdgcn_readfirstlane(sp.row0);
-      sp.end = __builtin_amdgcn_readfirstlane(sp.end);
-      return true;
+      sp.e = __builtin_amdgcn_readfirstlane(e0 + at);
+      sp.row0 = __builtin_amdgcn_readfirstlane(__shfl(lo + (mt - before - (incl - tiles)) * BM, at, 64));
+      sp.end = __builtin_amdgcn_readfirstlane(__shfl(hi, at, 64));
+      // offsets that no plan wrote may overlap and their tiles overflow: still only rows of this group
+      return sp.row0 >= __builtin_amdgcn_readfirstlane(__shfl(lo, at, 64)) && sp.row0 < sp.end;
     }
     before += __shfl(incl, 63, 64);
   }
@@ -396,7 +394,7 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t
 template <bool GATED>
 __global__ __launch_bounds__(512) void q8_big_kernel(Q8Args a, int32_t nt, int32_t mt_count) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * 512 * kStep];
-  if (a.experts) mt_count = count_spans<256>(a);  // the launch has room for the bound
+  if (a.experts) mt_count = max(0, min(count_spans<256>(a), mt_count));  // the launch has room for the bound
   const int32_t total = mt_count * nt;
   const int32_t rest = total % 256;
   const int32_t full = rest <= 128 ? total - rest : total;  // ids from the next multiple of 8 on are halves

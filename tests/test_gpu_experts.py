@@ -143,6 +143,14 @@ def test_groups_outside_the_buffer_are_bounded(vq):
                            cu(s_in), None, 64, 6, gated=True, out=guard[2:8])
         torch.cuda.synchronize()
         assert bool((guard[:2] == 7.0).all()) and bool((guard[8:] == 7.0).all())
+    # the same with the large tiles: groups that overlap ask for more tiles than the launch holds
+    rows = torch.zeros(900, dtype=torch.int32, device="cuda")
+    for off in ([0, 900, 5, 900], [900, 0, 900, 100], [-2 ** 31, 2 ** 31 - 1, -1, 2 ** 31 - 1]):
+        guard = torch.full((904, 32), 7.0, device="cuda")
+        vq.q8_gemm_grouped(cu(np.array(off, np.int64).astype(np.int32)), rows, q, s, vq.q8_pad(cu(w_in)), cu(s_in),
+                           None, 64, 900, gated=True, out=guard[2:902])
+        torch.cuda.synchronize()
+        assert bool((guard[:2] == 7.0).all()) and bool((guard[902:] == 7.0).all())
 
 
 @pytest.mark.parametrize("t,top,n", [(1, 1, 1), (3, 2, 5), (40, 4, 130), (300, 2, 1027), (2, 8, 4096)])
