@@ -1,6 +1,10 @@
 // The 8-bit products: y[m][n] = (sum_k q[m][k] w[n][k]) s[m] sw[n] (+ bias[n]), dense (vq_q8_gemm) and grouped by
 // expert (vq_q8_gemm_grouped), on the int8 matrix instructions with exact int32 sums.
 //
+// Up to some hundred rows the weights' bytes bound it (one row of 28672 x 8192: 48 us, 4.9 TB/s), above that the matrix
+// pipes at the clock that the card holds under dense 8-bit products (8192^3: 2.2 - 2.4 POP/s on random values, 3.4 on
+// zeros).
+//
 // Rows of q and w are whole 128-byte steps with zero pads, so no kernel has a K edge; rows past an edge of a tile read
 // the last valid row again and are not stored.  Sums of integers have no order, so nothing here depends on how K is cut.
 #include <algorithm>
@@ -141,6 +145,7 @@ __device__ __forceinline__ void to_lds(const uint8_t* g, uint8_t* l) {
 
 // The workgroup's barrier alone.  __syncthreads() would also wait for every load to LDS that is still on its way; here
 // each wavefront has waited for those that the others need, and for its own reads, and no memory operation moves across.
+// 64 x 8192 x 8192 in 64 x 128 tiles of three steps: 53 us with __syncthreads(), 34 us.
 __device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
