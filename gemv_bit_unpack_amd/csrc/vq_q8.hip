@@ -154,11 +154,12 @@ __device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
 }
 
-// One tile: WM x WN wavefronts compute BM rows (from row0, those below end) by BN weight rows (with the gate: BN / 2
+// One tile: KG groups of WM x WN wavefronts, each with its share of K and its own steps in LDS, compute BM rows (from
+// row0, those below end) by BN weight rows (with the gate: BN / 2
 // outputs, 32-row blocks of gate and up rows in turn, so that a lane ends with both values of an output).  The weights
 // are the matrix instruction's first operand: a lane then holds 16 outputs of one token, and since block row i holds
 // weight row perm(i) they are 16 consecutive ones.
-template <int BM, int BN, int WM, int WN, int NB, bool GATED, bool SPLIT>
+template <int BM, int BN, int WM, int WN, int NB, int KG, bool GATED, bool SPLIT>
 __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0, uint8_t* lds) {
   constexpr int kWaves = WM * WN;
   constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
@@ -171,9 +172,12 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
   constexpr int kWaitNext = 0x0070 | (kLater & 15) | (kLater >> 4) << 14;  // and lgkmcnt(0)
   static_assert(TL * 8 * kWaves == BM && WL * 8 * kWaves == BN, "whole loads");
   static_assert(!GATED || NI % 2 == 0, "gate and up blocks in one wavefront");
+  static_assert(KG == 1 || (KG == 2 && MI == 1 && NI == 1), "two groups of wavefronts halve K for single blocks");
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = all_wave % kWaves, group = all_wave / kWaves;
+  lds += group * NB * kBuf;
   const int64_t ld = vqi::q8_row_bytes(a.k);
   const int64_t wrows = GATED ? 2 * (int64_t)a.n : a.n;
   const uint8_t* const w = a.w + (int64_t)sp.e * wrows * ld;
@@ -184,6 +188,11 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
     kt0 = (int32_t)((int64_t)all * blockIdx.y / a.splits);
     kt1 = (int32_t)((int64_t)all * (blockIdx.y + 1) / a.splits);
   }
+
+  // steps of each group of wavefronts; the second may have one less, and multiplies zeros in its place
+  const int32_t n = (kt1 - kt0 + KG - 1) / KG;
+  kt0 += group * n;
+  const int32_t mine = KG == 1 ? n : min(n, kt1 - kt0);
 
   // this lane's 16-byte piece of every load: row p of the tile, chunk lane % 8 of its LDS row, which holds chunk
   // (lane % 8) ^ (p / 2 % 8) of the matrix row (reads of 16 rows at one chunk then fall on all 64 banks)
@@ -208,7 +217,13 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
     }
     gw[j] = w + r * ld + kt0 * kStep + (((lane & 7) ^ ((p >> 1) & 7)) * 16);
   }
-  auto fetch = [&](int buf) {
+  auto fetch = [&](int buf, int32_t step) {
+    if (KG > 1 && step >= mine) {
+#pragma unroll
+      for (int j = 0; j < TL; ++j)
+        *(v4i*)(lds + buf * kBuf + (j * kWaves + wave) * 1024 + lane * 16) = v4i{0, 0, 0, 0};
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < TL; ++j) {
       to_lds(gt[j], lds + buf * kBuf + (j * kWaves + wave) * 1024);
@@ -252,14 +267,14 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
 
 #pragma unroll
   for (int b = 0; b < NB; ++b)
-    if (b < NB - 1 && kt0 + b < kt1) fetch(b);
-  if (kt0 + NB - 1 <= kt1) {
+    if (b < NB - 1 && b < n) fetch(b, b);
+  if (NB - 1 <= mine) {
     __builtin_amdgcn_s_waitcnt(kWaitNext);  // this wavefront's part of the first step is in LDS
   } else {
     __builtin_amdgcn_s_waitcnt(0x0070);
   }
   meet();  // and everyone's
-  if (kt0 + NB - 1 < kt1) fetch(NB - 1);
+  if (NB - 1 < n) fetch(NB - 1, NB - 1);
   read(0, 0, 0);
   int buf = 0;
   auto mix = [&] {  // the reads of the next slice between the products of this one
@@ -282,16 +297,16 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
     read(1, buf, 3);
     mix();
   };
-  for (int32_t kt = kt0; kt + 1 < kt1; ++kt) {
+  for (int32_t kt = 0; kt + 1 < n; ++kt) {
     first3();
     // its part of the next step is in LDS (steps after that may still be on their way), its last reads are done
-    if (kt + NB - 1 < kt1) {
+    if (kt + NB - 1 < mine) {
       __builtin_amdgcn_s_waitcnt(kWaitNext);
     } else {
       __builtin_amdgcn_s_waitcnt(0x0070);
     }
     meet();  // and everyone's: the next step may be read, this one overwritten
-    if (kt + NB < kt1) fetch(buf);
+    if (kt + NB < n) fetch(buf, kt + NB);
     const int next = buf + 1 == NB ? 0 : buf + 1;
     __builtin_amdgcn_sched_barrier(0);
     multiply(1);
@@ -301,6 +316,23 @@ __device__ __forceinline__ void tile(const Q8Args& a, const Span& sp, int32_t n0
   }
   first3();
   multiply(1);
+  if constexpr (KG == 2) {  // the second group's sums join the first's
+    v4i* const sums = (v4i*)(lds + (1 - group) * NB * kBuf) + wave * 4 * 64 + lane;
+    meet();  // no one reads a step any more
+    if (group == 1) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        sums[r * 64] = v4i{acc[0][0][4 * r], acc[0][0][4 * r + 1], acc[0][0][4 * r + 2], acc[0][0][4 * r + 3]};
+    }
+    __syncthreads();
+    if (group == 1) return;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const v4i v = sums[r * 64];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[0][0][4 * r + k] += v[k];
+    }
+  }
 
   // outputs: lane = token row0 + .., 16 consecutive channels per block
 #pragma unroll
@@ -382,14 +414,14 @@ __device__ __forceinline__ bool place(int32_t id, int32_t total, int32_t mt_coun
 }
 
 // Tiles with several workgroups per CU.
-template <int BM, int BN, int WM, int WN, int NB, bool GATED, bool SPLIT>
-__global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a, int32_t nt, int32_t mt_count) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NB * (BM + BN) * kStep];
+template <int BM, int BN, int WM, int WN, int NB, int KG, bool GATED, bool SPLIT>
+__global__ __launch_bounds__(64 * WM * WN * KG) void q8_tile_kernel(Q8Args a, int32_t nt, int32_t mt_count) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NB * (BM + BN) * kStep];
   int32_t mt, nti;
   if (!place((int32_t)blockIdx.x, mt_count * nt, mt_count, nt, mt, nti)) return;
   Span sp{0, mt * BM, a.m};
   if (a.experts && !find_span<BM>(a, mt, sp)) return;
-  tile<BM, BN, WM, WN, NB, GATED, SPLIT>(a, sp, nti * (GATED ? BN / 2 : BN), lds);
+  tile<BM, BN, WM, WN, NB, KG, GATED, SPLIT>(a, sp, nti * (GATED ? BN / 2 : BN), lds);
 }
 
 // 256 x 256 tiles on 8 wavefronts, one workgroup per CU: half the LDS reads and half the matrix bytes per operation of
@@ -421,9 +453,9 @@ __global__ __launch_bounds__(512) void q8_big_kernel(Q8Args a, int32_t nt, int32
   if (sp.row0 >= sp.end) return;
   if (half) sp.end = min(sp.end, sp.row0 + 128);
   if (half || sp.end - sp.row0 <= 128) {
-    tile<128, 256, 2, 4, 2, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
+    tile<128, 256, 2, 4, 2, 1, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
   } else {
-    tile<256, 256, 2, 4, 2, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
+    tile<256, 256, 2, 4, 2, 1, GATED, false>(a, sp, nti * (GATED ? 128 : 256), lds);
   }
 }
 
@@ -815,15 +847,16 @@ vq_status launch_few_rows(const Q8Args& a, hipStream_t st) {
   }
 }
 
-template <int BM, int BN, int WM, int WN, int NB, bool GATED, bool SPLIT>
+template <int BM, int BN, int WM, int WN, int NB, int KG, bool GATED, bool SPLIT>
 vq_status launch_tile(const Q8Args& a, hipStream_t st) {
   const int out = GATED ? BN / 2 : BN;
   const int64_t mt = a.experts ? span_bound(a, BM) : ((int64_t)a.m + BM - 1) / BM;
   const int64_t nt = ((int64_t)a.n + out - 1) / out;
-  if (!vqi::grid_ok(mt * nt + 8, 64 * WM * WN)) return VQ_ERR_SHAPE;
+  constexpr int kThreads = 64 * WM * WN * KG;
+  if (!vqi::grid_ok(mt * nt + 8, kThreads)) return VQ_ERR_SHAPE;
   const uint32_t blocks = (uint32_t)((mt * nt + 7) / 8 * 8);
-  q8_tile_kernel<BM, BN, WM, WN, NB, GATED, SPLIT>
-      <<<dim3(blocks, SPLIT ? a.splits : 1), dim3(64 * WM * WN), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
+  q8_tile_kernel<BM, BN, WM, WN, NB, KG, GATED, SPLIT>
+      <<<dim3(blocks, SPLIT ? a.splits : 1), dim3(kThreads), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
 }
 vq_status launch_join(const Q8Args& a, hipStream_t st) {
@@ -886,23 +919,28 @@ vq_status launch_q8_one(const OneArgs& a, void* stream) {
 // in LDS: one step of a tile takes about a microsecond to arrive, so a CU with one workgroup moves what the workgroup
 // has on its way in that time.
 namespace {
-enum Way { kStreamed, k64x64, k128x64, k128x128, k128x128Pair, k256x256 };
+enum Way { kStreamed, k64x32, k64x64, k128x64, k128x128, k128x128Pair, k256x256 };
 struct Plan {
   Way way;
   int32_t splits;  // cuts of K over the CUs
 };
 Plan dense_plan(int32_t m, int32_t n, int32_t k) {
-  // us, rows x 5003 x 4099: 16 rows 11.2 streamed, 12.4 in 64 x 64; 48 rows 15.6 and 12.4.  14336 x 4096: 2 rows 16.5
-  // and 17.1, 32 rows 19.8 and 16.0
-  if (m <= 64 && (int64_t)m * n * k <= 600000000) return {kStreamed, 1};
+  // us, streamed and in the tiles that would be taken: 4096 x 4096, 16 rows 7.5 and 9.0, 48 rows 10.7 and 9.0;
+  // 5003 x 4099, 16 rows 11.2 and 10.2; 8192 x 8192, 16 rows 17.0 and 20.5; 4096 x 14336, 16 rows 20.0 and 17.2
+  const int64_t nk = (int64_t)n * k;
+  if (m <= 64 && (m * nk <= 400000000 || (m <= 16 && k <= 8192 && nk <= 70000000))) return {kStreamed, 1};
   const int64_t steps = q8_row_bytes(k) / kStep;
   auto tiles = [&](int bm, int bn) { return (((int64_t)m + bm - 1) / bm) * (((int64_t)n + bn - 1) / bn); };
   // K is cut where the tiles leave CUs without work, at 28 steps or more each: the int32 partial sums cost a second launch
   auto cut = [&](int64_t t) { return (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / t, steps / 28)); };
-  const int64_t small = tiles(64, 64), tall = tiles(128, 64), wide = tiles(128, 128);
+  const int64_t narrow = tiles(64, 32), small = tiles(64, 64), tall = tiles(128, 64), wide = tiles(128, 128);
   // 512 x 28672 x 8192 (224 of them): 117 us against 156 in 128 x 128; 1024 x 8192 x 8192 (128): 100 against 73
   if (tiles(256, 256) >= 200) return {k256x256, 1};
-  // 64 x 28672 x 8192: 53 us; 128 x 4096 x 4096: 11.8 against 15.0 in 128 x 64 and 22 in 128 x 128; 64 x 4096 x 14336:
+  // at most one for each CU, with two groups of wavefronts that halve K: 37 x 5003 x 4099 10.2 us (64 x 64: 12.8),
+  // 128 x 4096 x 4096 9.4 (12.0), 64 x 8192 x 8192 20.5 (22.5 cut in 4); 256 x 4096 x 4096, 512 of them, 16.4 (12.5);
+  // 64 x 4096 x 14336, 128 of them, 29.3 (20.3 cut in 4)
+  if (narrow <= 256 && (narrow > 128 || steps < 64)) return {k64x32, 1};
+  // 64 x 28672 x 8192: 53 us; 256 x 4096 x 4096: 12.5 against 15.1 in 128 x 64 and 23 in 128 x 128; 64 x 4096 x 14336:
   // 19.4 cut in 4, 37 uncut.  128 x 8192 x 28672, where each step counts: 82 us against 63 in 128 x 128 cut in 4
   if (m <= 64 || (small <= 256 && steps < 100)) return {k64x64, cut(small)};
   // 128 x 14336 x 4096: 20.8 us against 23.8 in 64 x 64 and 26.2 in 128 x 128; 256 x 8192 x 8192: 33.7, 41.4 and 37.8
@@ -928,30 +966,31 @@ vq_status launch_q8(const Q8Args& a, void* stream) {
     const int64_t groups = a.m < a.experts ? a.m : a.experts;
     const int64_t avg = (a.m + groups - 1) / groups;
     if (a.gated) {
-      if (avg <= 4) return launch_tile<32, 128, 1, 2, 2, true, false>(a, st);
-      if (avg <= 96) return launch_tile<64, 128, 2, 2, 2, true, false>(a, st);
-      return avg <= 192 ? launch_tile<128, 128, 2, 2, 2, true, false>(a, st) : launch_big<true>(a, st);
+      if (avg <= 4) return launch_tile<32, 128, 1, 2, 2, 1, true, false>(a, st);
+      if (avg <= 96) return launch_tile<64, 128, 2, 2, 2, 1, true, false>(a, st);
+      return avg <= 192 ? launch_tile<128, 128, 2, 2, 2, 1, true, false>(a, st) : launch_big<true>(a, st);
     }
-    if (avg <= 48) return launch_tile<32, 128, 1, 4, 2, false, false>(a, st);
-    return avg <= 192 ? launch_tile<128, 128, 2, 2, 2, false, false>(a, st) : launch_big<false>(a, st);
+    if (avg <= 48) return launch_tile<32, 128, 1, 4, 2, 1, false, false>(a, st);
+    return avg <= 192 ? launch_tile<128, 128, 2, 2, 2, 1, false, false>(a, st) : launch_big<false>(a, st);
   }
   switch (dense_plan(a.m, a.n, a.k).way) {
     case kStreamed:
       if (a.m <= 16) return launch_few_rows<1>(a, st);
       if (a.m <= 32) return launch_few_rows<2>(a, st);
       return a.m <= 48 ? launch_few_rows<3>(a, st) : launch_few_rows<4>(a, st);
+    case k64x32: return launch_tile<64, 32, 2, 1, 4, 2, false, false>(a, st);
     case k64x64: {
-      if (a.splits == 1) return launch_tile<64, 64, 2, 2, 4, false, false>(a, st);
-      const vq_status e = launch_tile<64, 64, 2, 2, 4, false, true>(a, st);
+      if (a.splits == 1) return launch_tile<64, 64, 2, 2, 4, 1, false, false>(a, st);
+      const vq_status e = launch_tile<64, 64, 2, 2, 4, 1, false, true>(a, st);
       return e != VQ_OK ? e : launch_join(a, st);
     }
-    case k128x64: return launch_tile<128, 64, 2, 2, 3, false, false>(a, st);
+    case k128x64: return launch_tile<128, 64, 2, 2, 3, 1, false, false>(a, st);
     case k128x128: {
-      if (a.splits == 1) return launch_tile<128, 128, 2, 2, 3, false, false>(a, st);
-      const vq_status e = launch_tile<128, 128, 2, 2, 3, false, true>(a, st);
+      if (a.splits == 1) return launch_tile<128, 128, 2, 2, 3, 1, false, false>(a, st);
+      const vq_status e = launch_tile<128, 128, 2, 2, 3, 1, false, true>(a, st);
       return e != VQ_OK ? e : launch_join(a, st);
     }
-    case k128x128Pair: return launch_tile<128, 128, 2, 2, 2, false, false>(a, st);
+    case k128x128Pair: return launch_tile<128, 128, 2, 2, 2, 1, false, false>(a, st);
     case k256x256: return launch_big<false>(a, st);
   }
   return VQ_ERR_UNSUPPORTED;
