@@ -467,17 +467,20 @@ __global__ __launch_bounds__(256) void q8_join_kernel(Q8Args a) {
   const int32_t m = (int32_t)(id / groups);
   const int32_t n = (int32_t)(id - (int64_t)m * groups) * 4;
   int32_t sum[4] = {0, 0, 0, 0};
-  for (int32_t k = 0; k < a.splits; ++k) {
-    const int32_t* p = a.part + ((int64_t)k * a.m + m) * a.n + n;
-    int32_t v[4] = {0, 0, 0, 0};
-    if (n + 4 <= a.n) {
-      __builtin_memcpy(v, p, 16);
-    } else {
+  const int64_t apart = (int64_t)a.m * a.n;
+  const int32_t* p = a.part + (int64_t)m * a.n + n;
+  if (n + 4 <= a.n) {
+#pragma unroll 8
+    for (int32_t k = 0; k < a.splits; ++k) {
+      int32_t v[4];
+      __builtin_memcpy(v, p + k * apart, 16);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = n + r < a.n ? p[r] : 0;
+      for (int r = 0; r < 4; ++r) sum[r] += v[r];
     }
+  } else {
+    for (int32_t k = 0; k < a.splits; ++k)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sum[r] += v[r];
+      for (int r = 0; r < 4; ++r) sum[r] += n + r < a.n ? p[k * apart + r] : 0;
   }
   float sc[4], b[4], v[4];
   load_run<4>(a.sw, n, a.n, sc);
@@ -927,22 +930,27 @@ struct Plan {
 Plan dense_plan(int32_t m, int32_t n, int32_t k) {
   // us, streamed and in the tiles that would be taken: 4096 x 4096, 16 rows 7.5 and 9.0, 48 rows 10.7 and 9.0;
   // 5003 x 4099, 16 rows 11.2 and 10.2; 8192 x 8192, 16 rows 17.0 and 20.5; 4096 x 14336, 16 rows 20.0 and 17.2
+  // (40 x 64 x 65536, four workgroups: 104 us streamed)
   const int64_t nk = (int64_t)n * k;
-  if (m <= 64 && (m * nk <= 400000000 || (m <= 16 && k <= 8192 && nk <= 70000000))) return {kStreamed, 1};
   const int64_t steps = q8_row_bytes(k) / kStep;
+  if (m <= 64 && (n >= 1024 || steps < 56) && (m * nk <= 400000000 || (m <= 16 && k <= 8192 && nk <= 70000000)))
+    return {kStreamed, 1};
   auto tiles = [&](int bm, int bn) { return (((int64_t)m + bm - 1) / bm) * (((int64_t)n + bn - 1) / bn); };
-  // K is cut where the tiles leave CUs without work, at 28 steps or more each: the int32 partial sums cost a second launch
-  auto cut = [&](int64_t t) { return (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / t, steps / 28)); };
+  // K is cut where the tiles leave CUs without work, if it is long enough to pay for the second launch (the int32 partial
+  // sums), and then over as many CUs as find 8 steps each
+  auto cut = [&](int64_t t) {
+    return steps < 56 ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / t, steps / 8));
+  };
   const int64_t narrow = tiles(64, 32), small = tiles(64, 64), tall = tiles(128, 64), wide = tiles(128, 128);
   // 512 x 28672 x 8192 (224 of them): 117 us against 156 in 128 x 128; 1024 x 8192 x 8192 (128): 100 against 73
   if (tiles(256, 256) >= 200) return {k256x256, 1};
   // at most one for each CU, with two groups of wavefronts that halve K: 37 x 5003 x 4099 10.2 us (64 x 64: 12.8),
   // 128 x 4096 x 4096 9.4 (12.0), 64 x 8192 x 8192 20.5 (22.5 cut in 4); 256 x 4096 x 4096, 512 of them, 16.4 (12.5);
-  // 64 x 4096 x 14336, 128 of them, 29.3 (20.3 cut in 4)
-  if (narrow <= 256 && (narrow > 128 || steps < 64)) return {k64x32, 1};
+  // 64 x 4096 x 14336, 128 of them, 29.3 (20.3 cut in 4); 64 x 8192 x 28672 68 (53 cut in 2)
+  if (narrow <= 256 && steps < (narrow > 128 ? 100 : 56)) return {k64x32, 1};
   // 64 x 28672 x 8192: 53 us; 256 x 4096 x 4096: 12.5 against 15.1 in 128 x 64 and 23 in 128 x 128; 64 x 4096 x 14336:
   // 19.4 cut in 4, 37 uncut.  128 x 8192 x 28672, where each step counts: 82 us against 63 in 128 x 128 cut in 4
-  if (m <= 64 || (small <= 256 && steps < 100)) return {k64x64, cut(small)};
+  if (m <= 64 || (small <= 256 && steps < (small > 128 ? 100 : 128))) return {k64x64, cut(small)};
   // 128 x 14336 x 4096: 20.8 us against 23.8 in 64 x 64 and 26.2 in 128 x 128; 256 x 8192 x 8192: 33.7, 41.4 and 37.8
   if (tall >= 160 && tall <= 256 && steps < 128) return {k128x64, 1};
   // 512 x 4096 x 4096: 17.0 us against 22.4 in 128 x 128

@@ -93,7 +93,8 @@ def test_quantize_row_stride_and_alignment(vq):
 SHAPES = [(1, 1, 1), (1, 16, 64), (1, 100, 130), (2, 17, 4096), (1, 4096, 4096), (5, 333, 1000), (16, 64, 14336),
           (17, 100, 256), (33, 65, 640), (37, 203, 4099), (64, 129, 2048), (65, 128, 128), (66, 257, 4096),
           (128, 130, 8192), (130, 1030, 200), (200, 1000, 300), (257, 640, 1152), (300, 4100, 520), (1000, 333, 777),
-          (2049, 384, 256), (5, 2, 65536), (70, 3, 65536)]
+          (2049, 384, 256), (5, 2, 65536), (70, 3, 65536), (138, 142, 17163), (100, 300, 7168), (60, 1100, 9000),
+          (300, 5003, 600), (257, 3000, 1025), (150, 9000, 640), (260, 17000, 257)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
