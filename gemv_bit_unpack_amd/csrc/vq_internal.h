@@ -218,7 +218,12 @@ struct OneArgs {
 };
 constexpr int32_t kQ8OneSlots = 8;            // most slots of the joined form
 constexpr size_t kQ8OneLds = 63 * 1024;       // most dynamic LDS of a workgroup
-size_t q8_one_lds(const OneArgs& a);
+// Dynamic LDS of the form that takes `a`: the 8-bit rows and the wavefronts' sums, two blocks of them unless joined.
+constexpr size_t q8_one_lds(int64_t slots, int32_t k, bool join) {
+  return (join ? slots : 1) * ((size_t)q8_row_bytes(k) + 8 * 64 * 16 * (join ? 1 : 2));
+}
+static_assert(q8_one_lds(1, VQ_Q8_ONE_MAX_K, false) <= kQ8OneLds && q8_one_lds(1, VQ_Q8_ONE_MAX_K + 1, false) > kQ8OneLds,
+              "the longest row that a dense product of one token keeps in LDS");
 vq_status launch_q8_one(const OneArgs& a, void* stream);
 
 // Routing (vq_experts.hip): ids [tokens * top] -> offsets [experts + 1], rows and pos [tokens * top].

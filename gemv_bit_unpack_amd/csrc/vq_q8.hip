@@ -885,11 +885,6 @@ vq_status launch_big(const Q8Args& a, hipStream_t st) {
 
 namespace vqi {
 
-size_t q8_one_lds(const OneArgs& a) {
-  const size_t slots = a.join ? a.slots : 1;
-  return slots * ((size_t)q8_row_bytes(a.k) + 8 * 64 * 16 * (a.join ? 1 : 2));
-}
-
 namespace {
 template <int RT, int WN, bool GATED, bool JOIN>
 vq_status launch_one_t(const OneArgs& a, hipStream_t st) {

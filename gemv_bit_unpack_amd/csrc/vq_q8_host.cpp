@@ -166,13 +166,14 @@ vq_status vq_q8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype 
   if (M < 0 || N < 0 || !valid_k(K) || ldx < K) return VQ_ERR_SHAPE;
   if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype)) return VQ_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return VQ_OK;
-  if (!x || !w || !sw || !y || !workspace) return VQ_ERR_NULL;
+  const bool one = M == 1 && K <= VQ_Q8_ONE_MAX_K;  // the kernel cuts the token itself
+  if (!x || !w || !sw || !y || (!workspace && !one)) return VQ_ERR_NULL;
   if (!aligned(x, size_of(x_dtype)) || !aligned(w, 16) || !aligned(sw, 4) || misaligned(bias, 2) ||
-      !aligned(y, size_of(y_dtype)) || !aligned(workspace, 256))
+      !aligned(y, size_of(y_dtype)) || misaligned(workspace, 256))
     return VQ_ERR_ALIGN;
   const LinearWs ws = linear_ws(M, N, K, workspace);
-  if (workspace_bytes < ws.bytes) return VQ_ERR_BUFFER_SIZE;
-  if (M == 1) {  // the kernel cuts the token itself
+  if (workspace && workspace_bytes < ws.bytes) return VQ_ERR_BUFFER_SIZE;
+  if (one) {
     OneArgs a;
     std::memset(&a, 0, sizeof a);
     a.n = N;
@@ -185,7 +186,7 @@ vq_status vq_q8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype 
     a.bias = (const uint16_t*)bias;
     a.y = y;
     a.y_dtype = y_dtype;
-    if (q8_one_lds(a) <= kQ8OneLds) return launch_q8_one(a, stream);
+    return launch_q8_one(a, stream);
   }
   const vq_status st = quantize(M, K, x, x_dtype, ldx, ws.q, ws.s, stream);
   if (st != VQ_OK) return st;
@@ -300,7 +301,7 @@ vq_status vq_q8_experts(int32_t tokens, int32_t top, int32_t experts, int32_t D,
     out.join = 1;
     out.y = y;
     out.y_dtype = y_dtype;
-    if (q8_one_lds(in) <= kQ8OneLds && q8_one_lds(out) <= kQ8OneLds) {
+    if (q8_one_lds(top, D, false) <= kQ8OneLds && q8_one_lds(top, I, true) <= kQ8OneLds) {
       if ((st = launch_q8_one(in, stream)) != VQ_OK) return st;
       return launch_q8_one(out, stream);
     }

@@ -11,7 +11,7 @@ Argument marshalling only, as in the package's ``__init__`` (which re-exports ev
     expert_combine(z, pos, p, y_dtype=..., out=None)
     q8_experts(x, ids, p, w_in, s_in, w_out, s_out, inner, ws, y_dtype=None, out=None)
     block_norm(z, residual=None, ...) -> (r, x) or (r, q, s)
-plus the layer objects ``Q8Linear`` and ``Q8Experts``, which keep a workspace per device and stream as ``VQLinear`` does.
+plus the layer objects ``Q8Linear`` and ``Q8Experts``, whose calls take a workspace of their own each.
 """
 from __future__ import annotations
 
@@ -19,6 +19,7 @@ import ctypes
 import functools
 
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+ONE_MAX_K = 48128  # VQ_Q8_ONE_MAX_K: up to this K one token's q8_linear takes no workspace
 _KINDS = {"none": NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
 
 
@@ -206,7 +207,8 @@ def q8_gemm(q, s, w, sw, bias, k, ws=None, y_dtype=None, out=None):
 
 
 def q8_linear(x, w, sw, bias, ws, y_dtype=None, out=None):
-    """q8_gemm on x [M, K] cut to 8 bits inside the call; ``ws``: a uint8 device buffer of q8_linear_workspace_bytes."""
+    """q8_gemm on x [M, K] cut to 8 bits inside the call; ``ws``: a uint8 device buffer of q8_linear_workspace_bytes
+    (None is taken for M = 1 and K <= ONE_MAX_K)."""
     torch = _torch()
     p, ld, code, dev = _rows(x, "x")
     (m, k), n = x.shape, w.shape[0]
@@ -352,19 +354,16 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
     return (r, q, s) if q8 else (r, x)
 
 
-_stream_ws = {}
+def _workspace(nbytes, like):
+    """(workspace on like's device, its pointer) for one call; (None, None) for 0 bytes.
 
-
-def _stream_workspace(nbytes, dev, stream):
-    """A workspace kept per (device, stream), grown on demand (None for 0 bytes)."""
+    A call is several launches that share it, so it belongs to that call alone: the allocator hands its memory out again
+    only behind these launches on their stream, gives calls of other threads other memory, and calls under capture memory
+    that the graph keeps."""
     if nbytes == 0:
-        return None
-    ws = _stream_ws.get((dev, stream))
-    if ws is None or ws.numel() < nbytes:
-        torch = _torch()
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
-        _stream_ws[(dev, stream)] = ws
-    return ws
+        return None, None
+    ws = like.new_empty(nbytes, dtype=_torch().uint8)
+    return ws, ws.data_ptr()
 
 
 def _tokens(x):
@@ -412,10 +411,10 @@ class Q8Linear:
             raise ValueError("x must be [..., %d] on device %d, got %s on %s" % (k, w.dev, tuple(x.shape), x.device))
         m, stream = rows.shape[0], _stream(dev)
         y = rows.new_empty((m, n), dtype=y_dtype or x.dtype)
-        nbytes = q8_linear_workspace_bytes(m, n, k)
-        ws = _stream_workspace(nbytes, dev, stream)
-        _check(lib().vq_q8_linear(m, n, k, p, code, ld, w.w, w.scale, w.bias, y.data_ptr(), _code(y.dtype),
-                                  None if ws is None else ws.data_ptr(), nbytes, stream), "vq_q8_linear")
+        nbytes = 0 if m == 1 and k <= ONE_MAX_K else q8_linear_workspace_bytes(m, n, k)
+        ws, ws_p = _workspace(nbytes, rows)
+        _check(lib().vq_q8_linear(m, n, k, p, code, ld, w.w, w.scale, w.bias, y.data_ptr(), _code(y.dtype), ws_p, nbytes,
+                                  stream), "vq_q8_linear")
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], n)
 
     __call__ = forward
@@ -426,10 +425,10 @@ class Q8Linear:
         m, stream = q.shape[0], _stream(w.dev)
         y = q.new_empty((m, n), dtype=y_dtype or torch.bfloat16)
         nbytes = q8_gemm_workspace_bytes(m, n, k)
-        ws = _stream_workspace(nbytes, w.dev, stream)
+        ws, ws_p = _workspace(nbytes, q)
         _check(lib().vq_q8_gemm(m, n, k, _ptr(q, "q", (m, q8_row_bytes(k)), w.dev, torch.int8),
                                 _ptr(s, "s", (m,), w.dev, torch.float32), w.w, w.scale, w.bias, y.data_ptr(),
-                                _code(y.dtype), None if ws is None else ws.data_ptr(), nbytes, stream), "vq_q8_gemm")
+                                _code(y.dtype), ws_p, nbytes, stream), "vq_q8_gemm")
         return y
 
 
@@ -460,11 +459,10 @@ class Q8Experts:
         t, top, stream = rows.shape[0], ids.shape[1], _stream(dev)
         y = rows.new_empty((t, d), dtype=y_dtype or x.dtype)
         nbytes = q8_experts_workspace_bytes(t, top, e, d, i)
-        ws = _stream_workspace(nbytes, dev, stream)
+        ws, ws_p = _workspace(nbytes, rows)
         _check(lib().vq_q8_experts(t, top, e, d, i, xp, code, ld, _ptr(ids, "ids", (t, top), dev, torch.int32),
                                    _ptr(p, "p", (t, top), dev, torch.float32), w.w_in, w.s_in, w.w_out, w.s_out,
-                                   y.data_ptr(), _code(y.dtype), None if ws is None else ws.data_ptr(), nbytes, stream),
-               "vq_q8_experts")
+                                   y.data_ptr(), _code(y.dtype), ws_p, nbytes, stream), "vq_q8_experts")
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], d)
 
     __call__ = forward

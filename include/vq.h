@@ -415,7 +415,8 @@ vq_status vq_q8_gemm(int32_t M, int32_t N, int32_t K, const void* q, const float
 
 /* vq_q8_gemm on x [M][K] (row stride ldx elements, fp16, bf16 or fp32) cut to 8 bits inside the call: the same y as
  * vq_q8_quantize followed by vq_q8_gemm.  The workspace is required where vq_q8_linear_workspace_bytes
- * is not 0. */
+ * is not 0, except for M = 1 and K <= VQ_Q8_ONE_MAX_K: one launch that uses none, NULL is taken. */
+#define VQ_Q8_ONE_MAX_K 48128
 vq_status vq_q8_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t* nbytes);
 vq_status vq_q8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype x_dtype, int64_t ldx, const void* w,
                        const float* sw, const void* bias, void* y, vq_dtype y_dtype, void* workspace,
