@@ -420,9 +420,6 @@ def assign(desc: Desc, w, cb1, cb2=None, ws=None, out1=None, out2=None):
     return out1, (out2 if desc.bits2 else None)
 
 
-_stream_ws = {}
-
-
 def rht_product_workspace_bytes(desc: Desc, m: int, x_dtype, gemm: bool) -> int:
     """Workspace bytes for gemv_ws_rht (gemm False) or gemm_ws_rht (gemm True)."""
     n = ctypes.c_size_t(0)
@@ -471,21 +468,14 @@ def gemm_ws_rht(desc, packed, cb1, cb2, scale, bias, x, signs, ws, y_dtype=None,
 
 
 def stream_workspace(desc: Desc, m: int, x_dtype, device, gemm_path: bool = False):
-    """A workspace kept per (device, current stream), grown on demand, for layers that run
-    their calls in stream order (gemv_ws, or gemm_ws with ``gemm_path``).  None when the
-    shape needs none."""
+    """A workspace for one call of a layer on the current stream (gemv_ws, or gemm_ws with
+    ``gemm_path``).  None when the shape needs none.
+
+    The allocator hands its memory out again only behind that call on its stream; calls of
+    other threads, and calls captured in a graph, have memory of their own."""
     torch = _torch()
     nbytes = (gemm_workspace_bytes if gemm_path else gemv_workspace_bytes)(desc, m, x_dtype)
-    if nbytes == 0:
-        return None
-    dev = torch.device(device)
-    key = (dev.index if dev.index is not None else torch.cuda.current_device(),
-           torch.cuda.current_stream(dev).cuda_stream)
-    ws = _stream_ws.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        _stream_ws[key] = ws
-    return ws
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 class VQLinear:
@@ -494,7 +484,7 @@ class VQLinear:
     ``forward(x)`` computes x W^T (+ bias) for x of shape [..., in_features]; batches of
     up to ``gemv_max_m`` rows take gemv_ws (the codebook-sliced kernel where the shape has
     it), larger ones gemm_ws (the matrix-core product fed by the gathering lanes where the
-    shape has it); both with a workspace kept per device and stream.  With
+    shape has it); both with a workspace of the call's own.  With
     ``decode_packed`` (the same indices in the slice-bucketed layout, ``decode_desc``) a
     batch of one row takes the bucketed decode product instead.
     """
