@@ -79,7 +79,8 @@ def _stream(dev):
 
 @functools.lru_cache(maxsize=1024)
 def _norm_desc(*fields):
-    """A vq_norm_desc, by reference (it is only read)."""
+    """A vq_norm_desc, by reference (it is only read); plain numbers only, which are what they compare as: a tensor would
+    be found again by its identity, with the value that it had then."""
     return ctypes.byref(NormDesc(*fields))
 
 
@@ -349,7 +350,8 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
         x = _like(z, x_dtype or z.dtype)
         x_p, x_code = x.data_ptr(), _code(x.dtype)
     desc = _norm_desc(m, d, *kinds, z_code, h_code, VQ_F32 if w_dtype is None else _code(w_dtype), gate_code, x_code,
-                      min(int(gate_rows), 2 ** 31 - 1), eps, weight_offset, res_scale, gate_scale, ldz, ldh)
+                      min(int(gate_rows), 2 ** 31 - 1), float(eps) + 0.0, float(weight_offset) + 0.0,
+                      float(res_scale) + 0.0, float(gate_scale) + 0.0, ldz, ldh)  # + 0.0: -0.0 is found as 0.0
     _check(lib().vq_block_norm(desc, zp, hp, *vecs, gate_p, r_p, x_p, q_p, s_p, _stream(dev)), "vq_block_norm")
     return (r, q, s) if q8 else (r, x)
 
