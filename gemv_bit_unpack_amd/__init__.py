@@ -25,6 +25,7 @@ Q8Experts.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -177,6 +178,7 @@ def pack(desc: Desc, idx1, idx2=None) -> np.ndarray:
 
 # ------------------------------------------------------------------ torch marshalling
 
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
 
@@ -211,20 +213,33 @@ def _stream_ptr(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _launch(fn, dev, *args):
+    """Library call `fn` with device index dev current, which a stream's handle does not say (every device's default
+    stream is handle 0); raises what the call refuses."""
+    c = _torch()._C
+    was = c._cuda_exchangeDevice(dev)
+    try:
+        status = fn(*args)
+    finally:
+        if was != dev:
+            c._cuda_maybeExchangeDevice(was)
+    if status != VQ_OK:
+        raise VQError(status, fn.__name__)
+
+
 def dequant(desc: Desc, packed, cb1, cb2, scale, w_dtype=None, out=None):
     torch = _torch()
     w_dtype = w_dtype or torch.float32
     if out is None:
         out = torch.empty((desc.out_features, desc.in_features), dtype=w_dtype, device=packed.device)
     f16 = (torch.float16,)
-    st = lib().vq_dequant(ctypes.byref(desc), _dev_ptr(packed, "packed"), _dev_ptr(cb1, "cb1", f16),
-                         _dev_ptr(cb2, "cb2", f16) if desc.bits2 else None, _dev_ptr(scale, "scale", f16),
-                         _dev_ptr(out, "out"), _dtype_code(out.dtype), _stream_ptr(packed.device))
-    _check(st, "vq_dequant")
+    _launch(lib().vq_dequant, packed.get_device(), ctypes.byref(desc), _dev_ptr(packed, "packed"),
+            _dev_ptr(cb1, "cb1", f16), _dev_ptr(cb2, "cb2", f16) if desc.bits2 else None, _dev_ptr(scale, "scale", f16),
+            _dev_ptr(out, "out"), _dtype_code(out.dtype), _stream_ptr(packed.device))
     return out
 
 
-def _product(fn, name, desc, packed, cb1, cb2, scale, bias, x, y_dtype, out, extra=()):
+def _product(fn, desc, packed, cb1, cb2, scale, bias, x, y_dtype, out, extra=()):
     torch = _torch()
     if x.dim() != 2 or x.shape[1] != desc.in_features:
         raise ValueError("x must be [M, %d], got %s" % (desc.in_features, tuple(x.shape)))
@@ -233,16 +248,15 @@ def _product(fn, name, desc, packed, cb1, cb2, scale, bias, x, y_dtype, out, ext
     if out is None:
         out = torch.empty((m, desc.out_features), dtype=y_dtype, device=x.device)
     f16 = (torch.float16,)
-    st = fn(ctypes.byref(desc), _dev_ptr(packed, "packed"), _dev_ptr(cb1, "cb1", f16),
+    _launch(fn, x.get_device(), ctypes.byref(desc), _dev_ptr(packed, "packed"), _dev_ptr(cb1, "cb1", f16),
             _dev_ptr(cb2, "cb2", f16) if desc.bits2 else None, _dev_ptr(scale, "scale", f16),
-            _dev_ptr(bias, "bias", f16), _dev_ptr(x, "x", (torch.float16, torch.bfloat16)), _dtype_code(x.dtype),
-            m, _dev_ptr(out, "out"), _dtype_code(out.dtype), *extra, _stream_ptr(x.device))
-    _check(st, name)
+            _dev_ptr(bias, "bias", f16), _dev_ptr(x, "x", (torch.float16, torch.bfloat16)), _dtype_code(x.dtype), m,
+            _dev_ptr(out, "out"), _dtype_code(out.dtype), *extra, _stream_ptr(x.device))
     return out
 
 
 def gemv(desc, packed, cb1, cb2, scale, bias, x, y_dtype=None, out=None):
-    return _product(lib().vq_gemv, "vq_gemv", desc, packed, cb1, cb2, scale, bias, x, y_dtype, out)
+    return _product(lib().vq_gemv, desc, packed, cb1, cb2, scale, bias, x, y_dtype, out)
 
 
 def gemv_workspace_bytes(desc: Desc, m: int, x_dtype) -> int:
@@ -266,18 +280,18 @@ def gemv_ws(desc, packed, cb1, cb2, scale, bias, x, ws, y_dtype=None, out=None):
 
     Calls that share a workspace must be ordered (one stream)."""
     extra = (None, 0) if ws is None else (_dev_ptr(ws, "workspace"), ws.numel() * ws.element_size())
-    return _product(lib().vq_gemv_ws, "vq_gemv_ws", desc, packed, cb1, cb2, scale, bias, x, y_dtype, out, extra)
+    return _product(lib().vq_gemv_ws, desc, packed, cb1, cb2, scale, bias, x, y_dtype, out, extra)
 
 
 def gemv_noalloc(desc, packed, cb1, cb2, scale, bias, x, y_dtype=None, out=None):
     """gemv_ws with the library's fixed per-GPU workspace: allocates nothing (``out`` given).
 
     Calls on one GPU share that workspace and must not overlap."""
-    return _product(lib().vq_gemv_noalloc, "vq_gemv_noalloc", desc, packed, cb1, cb2, scale, bias, x, y_dtype, out)
+    return _product(lib().vq_gemv_noalloc, desc, packed, cb1, cb2, scale, bias, x, y_dtype, out)
 
 
 def gemm(desc, packed, cb1, cb2, scale, bias, x, y_dtype=None, out=None):
-    return _product(lib().vq_gemm, "vq_gemm", desc, packed, cb1, cb2, scale, bias, x, y_dtype, out)
+    return _product(lib().vq_gemm, desc, packed, cb1, cb2, scale, bias, x, y_dtype, out)
 
 
 def gemm_workspace_bytes(desc: Desc, m: int, x_dtype) -> int:
@@ -301,7 +315,7 @@ def gemm_ws(desc, packed, cb1, cb2, scale, bias, x, ws, y_dtype=None, out=None):
 
     Calls that share a workspace must be ordered (one stream)."""
     extra = (None, 0) if ws is None else (_dev_ptr(ws, "workspace"), ws.numel() * ws.element_size())
-    return _product(lib().vq_gemm_ws, "vq_gemm_ws", desc, packed, cb1, cb2, scale, bias, x, y_dtype, out, extra)
+    return _product(lib().vq_gemm_ws, desc, packed, cb1, cb2, scale, bias, x, y_dtype, out, extra)
 
 
 def svq_desc(out_features, in_features) -> Desc:
@@ -330,24 +344,23 @@ def svq_dequant(desc: Desc, packed, a, b, scale, w_dtype=None, out=None):
     if out is None:
         out = torch.empty((desc.out_features, desc.in_features), dtype=w_dtype, device=packed.device)
     f16 = (torch.float16,)
-    st = lib().vq_svq_dequant(ctypes.byref(desc), _dev_ptr(packed, "packed"), _dev_ptr(a, "a", f16),
-                             _dev_ptr(b, "b", f16), _dev_ptr(scale, "scale", f16), _dev_ptr(out, "out"),
-                             _dtype_code(out.dtype), _stream_ptr(packed.device))
-    _check(st, "vq_svq_dequant")
+    _launch(lib().vq_svq_dequant, packed.get_device(), ctypes.byref(desc), _dev_ptr(packed, "packed"),
+            _dev_ptr(a, "a", f16), _dev_ptr(b, "b", f16), _dev_ptr(scale, "scale", f16), _dev_ptr(out, "out"),
+            _dtype_code(out.dtype), _stream_ptr(packed.device))
     return out
 
 
 def svq_gemv(desc: Desc, packed, a, b, scale, bias, x, y_dtype=None, out=None):
     """y [M, N] = x W^T (+ bias) of an affine-lattice layer, 1 <= M <= 16."""
-    return _svq_product(lib().vq_svq_gemv, "vq_svq_gemv", desc, packed, a, b, scale, bias, x, y_dtype, out)
+    return _svq_product(lib().vq_svq_gemv, desc, packed, a, b, scale, bias, x, y_dtype, out)
 
 
 def svq_gemm(desc: Desc, packed, a, b, scale, bias, x, y_dtype=None, out=None):
     """y [M, N] = x W^T (+ bias) of an affine-lattice layer on the matrix cores, any M."""
-    return _svq_product(lib().vq_svq_gemm, "vq_svq_gemm", desc, packed, a, b, scale, bias, x, y_dtype, out)
+    return _svq_product(lib().vq_svq_gemm, desc, packed, a, b, scale, bias, x, y_dtype, out)
 
 
-def _svq_product(fn, name, desc, packed, a, b, scale, bias, x, y_dtype, out):
+def _svq_product(fn, desc, packed, a, b, scale, bias, x, y_dtype, out):
     torch = _torch()
     if x.dim() != 2 or x.shape[1] != desc.in_features:
         raise ValueError("x must be [M, %d], got %s" % (desc.in_features, tuple(x.shape)))
@@ -356,11 +369,10 @@ def _svq_product(fn, name, desc, packed, a, b, scale, bias, x, y_dtype, out):
     if out is None:
         out = torch.empty((m, desc.out_features), dtype=y_dtype, device=x.device)
     f16 = (torch.float16,)
-    st = fn(ctypes.byref(desc), _dev_ptr(packed, "packed"), _dev_ptr(a, "a", f16), _dev_ptr(b, "b", f16),
-            _dev_ptr(scale, "scale", f16), _dev_ptr(bias, "bias", f16),
+    _launch(fn, x.get_device(), ctypes.byref(desc), _dev_ptr(packed, "packed"), _dev_ptr(a, "a", f16),
+            _dev_ptr(b, "b", f16), _dev_ptr(scale, "scale", f16), _dev_ptr(bias, "bias", f16),
             _dev_ptr(x, "x", (torch.float16, torch.bfloat16)), _dtype_code(x.dtype), m, _dev_ptr(out, "out"),
             _dtype_code(out.dtype), _stream_ptr(x.device))
-    _check(st, name)
     return out
 
 
@@ -381,10 +393,9 @@ def rht(x, signs, transpose=False, y_dtype=None, out=None):
     y_dtype = y_dtype or x.dtype
     if out is None:
         out = torch.empty((m, n), dtype=y_dtype, device=x.device)
-    st = lib().vq_rht(m, n, _dev_ptr(x, "x", (torch.float16, torch.bfloat16, torch.float32)), _dtype_code(x.dtype),
-                      _dev_ptr(signs, "signs"), int(bool(transpose)), _dev_ptr(out, "out"), _dtype_code(out.dtype),
-                      _stream_ptr(x.device))
-    _check(st, "vq_rht")
+    _launch(lib().vq_rht, x.get_device(), m, n, _dev_ptr(x, "x", (torch.float16, torch.bfloat16, torch.float32)),
+            _dtype_code(x.dtype), _dev_ptr(signs, "signs"), int(bool(transpose)), _dev_ptr(out, "out"),
+            _dtype_code(out.dtype), _stream_ptr(x.device))
     return out
 
 
@@ -411,12 +422,11 @@ def assign(desc: Desc, w, cb1, cb2=None, ws=None, out1=None, out2=None):
     if ws is None:
         ws = torch.empty(max(assign_workspace_bytes(desc), 256), dtype=torch.uint8, device=w.device)
     f16 = (torch.float16,)
-    st = lib().vq_assign(ctypes.byref(desc), _dev_ptr(w, "w", (torch.float16, torch.bfloat16, torch.float32)),
-                         _dtype_code(w.dtype), _dev_ptr(cb1, "cb1", f16),
-                         _dev_ptr(cb2, "cb2", f16) if desc.bits2 else None, _dev_ptr(out1, "idx1", (torch.int32,)),
-                         _dev_ptr(out2, "idx2", (torch.int32,)) if desc.bits2 else None, _dev_ptr(ws, "workspace"),
-                         ws.numel() * ws.element_size(), _stream_ptr(w.device))
-    _check(st, "vq_assign")
+    _launch(lib().vq_assign, w.get_device(), ctypes.byref(desc),
+            _dev_ptr(w, "w", (torch.float16, torch.bfloat16, torch.float32)), _dtype_code(w.dtype),
+            _dev_ptr(cb1, "cb1", f16), _dev_ptr(cb2, "cb2", f16) if desc.bits2 else None,
+            _dev_ptr(out1, "idx1", (torch.int32,)), _dev_ptr(out2, "idx2", (torch.int32,)) if desc.bits2 else None,
+            _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream_ptr(w.device))
     return out1, (out2 if desc.bits2 else None)
 
 
@@ -447,12 +457,11 @@ def _rht_product(gemm, desc, packed, cb1, cb2, scale, bias, x, signs, ws, y_dtyp
     f16 = (torch.float16,)
     name = "vq_gemm_ws_rht" if gemm else "vq_gemv_ws_rht"
     wsp, wsb = (None, 0) if ws is None else (_dev_ptr(ws, "workspace"), ws.numel() * ws.element_size())
-    st = getattr(lib(), name)(ctypes.byref(desc), _dev_ptr(packed, "packed"), _dev_ptr(cb1, "cb1", f16),
-                              _dev_ptr(cb2, "cb2", f16) if desc.bits2 else None, _dev_ptr(scale, "scale", f16),
-                              _dev_ptr(bias, "bias", f16), _dev_ptr(x, "x", (torch.float16, torch.bfloat16)),
-                              _dtype_code(x.dtype), m, _dev_ptr(signs, "signs", (torch.uint8,)), _dev_ptr(out, "out"),
-                              _dtype_code(out.dtype), wsp, wsb, _stream_ptr(x.device))
-    _check(st, name)
+    _launch(getattr(lib(), name), x.get_device(), ctypes.byref(desc), _dev_ptr(packed, "packed"),
+            _dev_ptr(cb1, "cb1", f16), _dev_ptr(cb2, "cb2", f16) if desc.bits2 else None, _dev_ptr(scale, "scale", f16),
+            _dev_ptr(bias, "bias", f16), _dev_ptr(x, "x", (torch.float16, torch.bfloat16)), _dtype_code(x.dtype), m,
+            _dev_ptr(signs, "signs", (torch.uint8,)), _dev_ptr(out, "out"), _dtype_code(out.dtype), wsp, wsb,
+            _stream_ptr(x.device))
     return out
 
 

@@ -56,7 +56,7 @@ def bind(lib):
     lib.vq_q8_row_bytes.restype = i64
 
 
-from . import VQ_BF16, VQ_F16, VQ_F32, _check, _torch, lib  # noqa: E402
+from . import VQ_BF16, VQ_F16, VQ_F32, _check, _launch, _torch, lib  # noqa: E402
 
 _codes = {}
 
@@ -166,8 +166,8 @@ def q8_quantize(x, out=None):
     row = q8_row_bytes(k)
     q, s = out or (None, None)
     q, s = _out(q, (m, row), torch.int8, x), _out(s, (m,), torch.float32, x)
-    _check(lib().vq_q8_quantize(m, k, p, code, ld, _ptr(q, "q", (m, row), dev, torch.int8),
-                                _ptr(s, "s", (m,), dev, torch.float32), _stream(dev)), "vq_q8_quantize")
+    _launch(lib().vq_q8_quantize, dev, m, k, p, code, ld, _ptr(q, "q", (m, row), dev, torch.int8),
+            _ptr(s, "s", (m,), dev, torch.float32), _stream(dev))
     return q, s
 
 
@@ -200,10 +200,10 @@ def q8_gemm(q, s, w, sw, bias, k, ws=None, y_dtype=None, out=None):
     m, n, row = q.shape[0], w.shape[0], q8_row_bytes(k)
     out = _out(out, (m, n), y_dtype or torch.bfloat16, q)
     f32 = torch.float32
-    _check(lib().vq_q8_gemm(m, n, k, _ptr(q, "q", (m, row), dev, torch.int8), _ptr(s, "s", (m,), dev, f32),
-                            _ptr(w, "w", (n, row), dev, torch.int8), _ptr(sw, "sw", (n,), dev, f32),
-                            _ptr(bias, "bias", (n,), dev, torch.float16), _ptr(out, "out", (m, n), dev),
-                            _code(out.dtype), *_ws(ws, dev), _stream(dev)), "vq_q8_gemm")
+    _launch(lib().vq_q8_gemm, dev, m, n, k, _ptr(q, "q", (m, row), dev, torch.int8), _ptr(s, "s", (m,), dev, f32),
+            _ptr(w, "w", (n, row), dev, torch.int8), _ptr(sw, "sw", (n,), dev, f32),
+            _ptr(bias, "bias", (n,), dev, torch.float16), _ptr(out, "out", (m, n), dev), _code(out.dtype),
+            *_ws(ws, dev), _stream(dev))
     return out
 
 
@@ -214,10 +214,9 @@ def q8_linear(x, w, sw, bias, ws, y_dtype=None, out=None):
     p, ld, code, dev = _rows(x, "x")
     (m, k), n = x.shape, w.shape[0]
     out = _out(out, (m, n), y_dtype or x.dtype, x)
-    _check(lib().vq_q8_linear(m, n, k, p, code, ld, _ptr(w, "w", (n, q8_row_bytes(k)), dev, torch.int8),
-                              _ptr(sw, "sw", (n,), dev, torch.float32), _ptr(bias, "bias", (n,), dev, torch.float16),
-                              _ptr(out, "out", (m, n), dev), _code(out.dtype), *_ws(ws, dev), _stream(dev)),
-           "vq_q8_linear")
+    _launch(lib().vq_q8_linear, dev, m, n, k, p, code, ld, _ptr(w, "w", (n, q8_row_bytes(k)), dev, torch.int8),
+            _ptr(sw, "sw", (n,), dev, torch.float32), _ptr(bias, "bias", (n,), dev, torch.float16),
+            _ptr(out, "out", (m, n), dev), _code(out.dtype), *_ws(ws, dev), _stream(dev))
     return out
 
 
@@ -231,8 +230,8 @@ def expert_plan(ids, experts: int):
     # refused sizes are the library's to name; it is given no buffer for them
     offsets = ids.new_empty((max(int(experts), 0) + 1,), dtype=torch.int32)
     rows, pos = ids.new_empty((t * top,), dtype=torch.int32), ids.new_empty((t, top), dtype=torch.int32)
-    _check(lib().vq_expert_plan(t, top, int(experts), _ptr(ids, "ids", (t, top), dev, torch.int32), offsets.data_ptr(),
-                                rows.data_ptr(), pos.data_ptr(), _stream(dev)), "vq_expert_plan")
+    _launch(lib().vq_expert_plan, dev, t, top, int(experts), _ptr(ids, "ids", (t, top), dev, torch.int32),
+            offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(), _stream(dev))
     return offsets, rows, pos
 
 
@@ -249,12 +248,11 @@ def q8_gemm_grouped(offsets, rows, q, s, w, sw, bias, k, max_rows, gated=False, 
         raise ValueError("rows must have at least max_rows = %d entries, got %d" % (max_rows, rows.numel()))
     out = _out(out, (max_rows, n), y_dtype or torch.float32, q)
     i8, i32, f32 = torch.int8, torch.int32, torch.float32
-    _check(lib().vq_q8_gemm_grouped(e, max_rows, t, n, k, _ptr(offsets, "offsets", (e + 1,), dev, i32),
-                                    _ptr(rows, "rows", None, dev, i32), _ptr(q, "q", (t, row), dev, i8),
-                                    _ptr(s, "s", (t,), dev, f32), _ptr(w, "w", (e, nw, row), dev, i8),
-                                    _ptr(sw, "sw", (e, nw), dev, f32), _ptr(bias, "bias", (e, nw), dev, torch.float16),
-                                    int(bool(gated)), _ptr(out, "out", (max_rows, n), dev), _code(out.dtype),
-                                    _stream(dev)), "vq_q8_gemm_grouped")
+    _launch(lib().vq_q8_gemm_grouped, dev, e, max_rows, t, n, k, _ptr(offsets, "offsets", (e + 1,), dev, i32),
+            _ptr(rows, "rows", None, dev, i32), _ptr(q, "q", (t, row), dev, i8), _ptr(s, "s", (t,), dev, f32),
+            _ptr(w, "w", (e, nw, row), dev, i8), _ptr(sw, "sw", (e, nw), dev, f32),
+            _ptr(bias, "bias", (e, nw), dev, torch.float16), int(bool(gated)), _ptr(out, "out", (max_rows, n), dev),
+            _code(out.dtype), _stream(dev))
     return out
 
 
@@ -264,10 +262,9 @@ def expert_combine(z, pos, p, y_dtype=None, out=None):
     dev = _device(pos, "pos")
     (t, top), (r, n) = pos.shape, z.shape
     out = _out(out, (t, n), y_dtype or torch.float32, pos)
-    _check(lib().vq_expert_combine(t, top, n, r, _ptr(z, "z", (r, n), dev, torch.float32),
-                                   _ptr(pos, "pos", (t, top), dev, torch.int32),
-                                   _ptr(p, "p", (t, top), dev, torch.float32), _ptr(out, "out", (t, n), dev),
-                                   _code(out.dtype), _stream(dev)), "vq_expert_combine")
+    _launch(lib().vq_expert_combine, dev, t, top, n, r, _ptr(z, "z", (r, n), dev, torch.float32),
+            _ptr(pos, "pos", (t, top), dev, torch.int32), _ptr(p, "p", (t, top), dev, torch.float32),
+            _ptr(out, "out", (t, n), dev), _code(out.dtype), _stream(dev))
     return out
 
 
@@ -283,13 +280,11 @@ def q8_experts(x, ids, p, w_in, s_in, w_out, s_out, inner, ws, y_dtype=None, out
     top = ids.shape[1]
     out = _out(out, (t, d), y_dtype or x.dtype, x)
     i8, f32 = torch.int8, torch.float32
-    _check(lib().vq_q8_experts(t, top, e, d, inner, xp, code, ld, _ptr(ids, "ids", (t, top), dev, torch.int32),
-                               _ptr(p, "p", (t, top), dev, f32),
-                               _ptr(w_in, "w_in", (e, 2 * inner, q8_row_bytes(d)), dev, i8),
-                               _ptr(s_in, "s_in", (e, 2 * inner), dev, f32),
-                               _ptr(w_out, "w_out", (e, d, q8_row_bytes(inner)), dev, i8),
-                               _ptr(s_out, "s_out", (e, d), dev, f32), _ptr(out, "out", (t, d), dev),
-                               _code(out.dtype), *_ws(ws, dev), _stream(dev)), "vq_q8_experts")
+    _launch(lib().vq_q8_experts, dev, t, top, e, d, inner, xp, code, ld, _ptr(ids, "ids", (t, top), dev, torch.int32),
+            _ptr(p, "p", (t, top), dev, f32), _ptr(w_in, "w_in", (e, 2 * inner, q8_row_bytes(d)), dev, i8),
+            _ptr(s_in, "s_in", (e, 2 * inner), dev, f32), _ptr(w_out, "w_out", (e, d, q8_row_bytes(inner)), dev, i8),
+            _ptr(s_out, "s_out", (e, d), dev, f32), _ptr(out, "out", (t, d), dev), _code(out.dtype), *_ws(ws, dev),
+            _stream(dev))
     return out
 
 
@@ -352,7 +347,7 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
     desc = _norm_desc(m, d, *kinds, z_code, h_code, VQ_F32 if w_dtype is None else _code(w_dtype), gate_code, x_code,
                       min(int(gate_rows), 2 ** 31 - 1), float(eps) + 0.0, float(weight_offset) + 0.0,
                       float(res_scale) + 0.0, float(gate_scale) + 0.0, ldz, ldh)  # + 0.0: -0.0 is found as 0.0
-    _check(lib().vq_block_norm(desc, zp, hp, *vecs, gate_p, r_p, x_p, q_p, s_p, _stream(dev)), "vq_block_norm")
+    _launch(lib().vq_block_norm, dev, desc, zp, hp, *vecs, gate_p, r_p, x_p, q_p, s_p, _stream(dev))
     return (r, q, s) if q8 else (r, x)
 
 
@@ -415,8 +410,8 @@ class Q8Linear:
         y = rows.new_empty((m, n), dtype=y_dtype or x.dtype)
         nbytes = 0 if m == 1 and k <= ONE_MAX_K else q8_linear_workspace_bytes(m, n, k)
         ws, ws_p = _workspace(nbytes, rows)
-        _check(lib().vq_q8_linear(m, n, k, p, code, ld, w.w, w.scale, w.bias, y.data_ptr(), _code(y.dtype), ws_p, nbytes,
-                                  stream), "vq_q8_linear")
+        _launch(lib().vq_q8_linear, dev, m, n, k, p, code, ld, w.w, w.scale, w.bias, y.data_ptr(), _code(y.dtype), ws_p,
+                nbytes, stream)
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], n)
 
     __call__ = forward
@@ -428,9 +423,9 @@ class Q8Linear:
         y = q.new_empty((m, n), dtype=y_dtype or torch.bfloat16)
         nbytes = q8_gemm_workspace_bytes(m, n, k)
         ws, ws_p = _workspace(nbytes, q)
-        _check(lib().vq_q8_gemm(m, n, k, _ptr(q, "q", (m, q8_row_bytes(k)), w.dev, torch.int8),
-                                _ptr(s, "s", (m,), w.dev, torch.float32), w.w, w.scale, w.bias, y.data_ptr(),
-                                _code(y.dtype), ws_p, nbytes, stream), "vq_q8_gemm")
+        _launch(lib().vq_q8_gemm, w.dev, m, n, k, _ptr(q, "q", (m, q8_row_bytes(k)), w.dev, torch.int8),
+                _ptr(s, "s", (m,), w.dev, torch.float32), w.w, w.scale, w.bias, y.data_ptr(), _code(y.dtype), ws_p,
+                nbytes, stream)
         return y
 
 
@@ -462,9 +457,9 @@ class Q8Experts:
         y = rows.new_empty((t, d), dtype=y_dtype or x.dtype)
         nbytes = q8_experts_workspace_bytes(t, top, e, d, i)
         ws, ws_p = _workspace(nbytes, rows)
-        _check(lib().vq_q8_experts(t, top, e, d, i, xp, code, ld, _ptr(ids, "ids", (t, top), dev, torch.int32),
-                                   _ptr(p, "p", (t, top), dev, torch.float32), w.w_in, w.s_in, w.w_out, w.s_out,
-                                   y.data_ptr(), _code(y.dtype), ws_p, nbytes, stream), "vq_q8_experts")
+        _launch(lib().vq_q8_experts, dev, t, top, e, d, i, xp, code, ld, _ptr(ids, "ids", (t, top), dev, torch.int32),
+                _ptr(p, "p", (t, top), dev, torch.float32), w.w_in, w.s_in, w.w_out, w.s_out, y.data_ptr(),
+                _code(y.dtype), ws_p, nbytes, stream)
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], d)
 
     __call__ = forward
