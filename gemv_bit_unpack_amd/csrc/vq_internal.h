@@ -216,7 +216,9 @@ struct OneArgs {
   void* y;
   vq_dtype y_dtype;
 };
-constexpr int32_t kQ8OneSlots = 8;            // most slots of the joined form
+// Most slots of the joined form, which keeps all their rows in LDS: 7 of up to 1024 columns, 6 of 2560, 5 of 4608, 4 of
+// 7936, 3 of 13312, 2 of 24064.  More slots or longer rows take the grouped products.
+constexpr int32_t kQ8OneSlots = 7;
 constexpr size_t kQ8OneLds = 63 * 1024;       // most dynamic LDS of a workgroup
 // Dynamic LDS of the form that takes `a`: the 8-bit rows and the wavefronts' sums, two blocks of them unless joined.
 constexpr size_t q8_one_lds(int64_t slots, int32_t k, bool join) {
@@ -224,6 +226,8 @@ constexpr size_t q8_one_lds(int64_t slots, int32_t k, bool join) {
 }
 static_assert(q8_one_lds(1, VQ_Q8_ONE_MAX_K, false) <= kQ8OneLds && q8_one_lds(1, VQ_Q8_ONE_MAX_K + 1, false) > kQ8OneLds,
               "the longest row that a dense product of one token keeps in LDS");
+static_assert(q8_one_lds(kQ8OneSlots, 1, true) <= kQ8OneLds && q8_one_lds(kQ8OneSlots + 1, 1, true) > kQ8OneLds,
+              "as many slots as some row length finds room for");
 vq_status launch_q8_one(const OneArgs& a, void* stream);
 
 // Routing (vq_experts.hip): ids [tokens * top] -> offsets [experts + 1], rows and pos [tokens * top].

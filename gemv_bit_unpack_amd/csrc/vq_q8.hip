@@ -597,7 +597,8 @@ __global__ __launch_bounds__(512) void q8_few_kernel(Q8Args a) {
 // launch.  Weights go to the matrix instruction as in q8_few_kernel, with the token in all 16 columns.
 //   dense   y = the product                                        w [n]
 //   GATED   slot blockIdx.y: y[slot] = silu(g) u, fp32             w [experts][2 n], expert ids[slot], the same x for all
-//   JOIN    y = sum over slots of p[slot] * product(x row slot)    w [experts][n], experts ids[slot]
+//   JOIN    y = sum over slots of p[slot] * product(x row slot)    w [experts][n], experts ids[slot]; the rows of all
+//           slots are in LDS, so there is a bound on slots and columns together (kQ8OneSlots)
 // Slots whose id is outside [0, experts) are left out.
 // Bound by the weights' bytes (28672 x 8192: 48 us, 4.9 TB/s); a small matrix by the chain row -> scale -> 8 bits ->
 // products (4096 x 4096: 6.6 us; cutting the row in a launch of its own made it 3.0 + 5.3 us and a gap).

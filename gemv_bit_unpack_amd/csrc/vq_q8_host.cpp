@@ -275,7 +275,7 @@ vq_status vq_q8_experts(int32_t tokens, int32_t top, int32_t experts, int32_t D,
   const ExpertsWs ws = experts_ws(tokens, top, experts, D, I, workspace);
   if (workspace_bytes < ws.bytes) return VQ_ERR_BUFFER_SIZE;
   const int32_t pairs = tokens * top;
-  if (tokens == 1 && top <= kQ8OneSlots) {  // no routing to sort: two launches
+  if (tokens == 1 && top <= kQ8OneSlots) {  // no routing to sort: two launches, where the hidden rows fit LDS together
     OneArgs in, out;
     std::memset(&in, 0, sizeof in);
     in.slots = top;
