@@ -364,10 +364,13 @@ def _workspace(nbytes, like):
 
 
 def _tokens(x):
-    """x [..., K] as rows [M, K] (copied only where its rows are not contiguous)."""
+    """x [..., K] as rows [M, K] (copied only where its rows are not contiguous, or overlap as those of an expanded view)."""
     if x.dim() != 2:
         x = x.reshape(-1, x.shape[-1])
-    return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
+    if x.is_contiguous():
+        return x
+    (m, k), (ld, one) = x.shape, x.stride()
+    return x if (one == 1 or k <= 1) and (ld >= k or m <= 1) else x.contiguous()
 
 
 class _Weights:
