@@ -295,10 +295,23 @@ def block_norm(z, residual=None, *, post="none", post_weight=None, post_bias=Non
 
         r = res_scale * residual + gate_scale * gate * N_post(z),    x = N_pre(r)
 
-    z, residual [M, D] (any row strides); post / pre: "none", "rms" or "layer"; weights and biases [D]; gate [D], or
-    [ceil(M / gate_rows), D] with one row for every gate_rows rows.  Returns (r, x), or with ``q8`` (r, q, s): x in
-    8 bits.  r has the residual's dtype (z's without one); ``r_out`` may be the residual itself; ``keep_r=False``
-    returns None for it.  x_dtype defaults to z's."""
+    z, residual [M, D] (any row strides) or [..., D], M rows in all; post / pre: "none", "rms" or "layer"; weights and
+    biases [D]; gate [D], or [ceil(M / gate_rows), D] with one row for every gate_rows rows.  Returns (r, x) of z's shape,
+    or with ``q8`` (r, q, s): x in 8 bits, M rows.  r has the residual's dtype (z's without one); ``r_out`` may be the
+    residual itself; ``keep_r=False`` returns None for it.  x_dtype defaults to z's."""
+    if z.dim() > 2 or z.dim() == 1:
+        for what, t in (("residual", residual), ("r_out", r_out)):
+            if t is not None and t.shape != z.shape:
+                raise ValueError("%s must be %s, got %s" % (what, list(z.shape), tuple(t.shape)))
+        if r_out is not None and not r_out.is_contiguous():
+            raise ValueError("r_out must be contiguous")
+        flat = lambda t: None if t is None else _tokens(t)
+        r, *x = block_norm(flat(z), flat(residual), post=post, post_weight=post_weight, post_bias=post_bias, pre=pre,
+                           pre_weight=pre_weight, pre_bias=pre_bias, gate=gate, gate_rows=gate_rows, res_scale=res_scale,
+                           gate_scale=gate_scale, eps=eps, weight_offset=weight_offset, x_dtype=x_dtype, q8=q8,
+                           r_out=flat(r_out), keep_r=keep_r)
+        r = r_out if r is None or r_out is not None else r.reshape(z.shape)
+        return (r, *x) if q8 else (r, x[0].reshape(z.shape))
     kinds = _KINDS.get(post), _KINDS.get(pre)
     if None in kinds:
         raise ValueError("post and pre must be one of %s" % (tuple(_KINDS),))
