@@ -966,19 +966,26 @@ int32_t q8_splits(int32_t m, int32_t n, int32_t k) { return dense_plan(m, n, k).
 vq_status launch_q8(const Q8Args& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   if (a.experts) {
-    // rows of a group on average (in the larger of max_rows' bound): short groups take small tiles.  Gated and plain
-    // product in us, 64 experts of 2048 x 1024, 4 of them for a token, with 32-, 64-, 128- and 256-row tiles:
-    //   333 tokens 54 + 29, 54 + 33, 63 + 36, 67 + 42;  2000 tokens 112 + 59, 100 + 57, 99 + 64, 109 + 85
-    // 8 experts of 4096 x 14336, 2 for a token: 1000 tokens 617 + 346, 508 + 291, 433 + 242, 414 + 197
+    // Rows of a group on average (in the larger of max_rows' bound): short groups take small tiles, in between the plain
+    // product takes 128-row tiles while the CUs hold them all at once.  us, gated and plain product in 32-, 64-, 128- and
+    // 256-row tiles, rows of a group on average in front:
+    //   64 experts of 2048 x 1024     21: 51 + 29, 50 + 33, 58 + 37, 61 + 41      75: 90 + 46, 77 + 48, 88 + 59, 79 + 65
+    //                                125: 124 + 62, 101 + 60, 104 + 70, 105 + 83  188: 167 + 84, 128 + 78, 132 + 86, 117 + 92
+    //    8 experts of 4096 x 14336     4: 159 + 110, 167 + 113, 179 + 118, 181 + 139
+    //      (plain: 256 tiles of 128)  50: 265 + 159, 227 + 129, 235 + 132, 223 + 159
+    //                                125: 445 + 238, 332 + 159, 321 + 143, 280 + 183   250: 625 + 345, 520 + 296, 444 + 250, 384 + 195
+    //   32 experts of 1536 x 5000    100: 212 + 99, 177 + 88, 188 + 99, 176 + 76
     const int64_t groups = a.m < a.experts ? a.m : a.experts;
     const int64_t avg = (a.m + groups - 1) / groups;
     if (a.gated) {
       if (avg <= 4) return launch_tile<32, 128, 1, 2, 2, 1, true, false>(a, st);
-      if (avg <= 96) return launch_tile<64, 128, 2, 2, 2, 1, true, false>(a, st);
-      return avg <= 192 ? launch_tile<128, 128, 2, 2, 2, 1, true, false>(a, st) : launch_big<true>(a, st);
+      return avg <= 96 ? launch_tile<64, 128, 2, 2, 2, 1, true, false>(a, st) : launch_big<true>(a, st);
     }
     if (avg <= 48) return launch_tile<32, 128, 1, 4, 2, 1, false, false>(a, st);
-    return avg <= 192 ? launch_tile<128, 128, 2, 2, 2, 1, false, false>(a, st) : launch_big<false>(a, st);
+    if (avg > 192) return launch_big<false>(a, st);
+    return (avg + 127) / 128 * groups * (((int64_t)a.n + 127) / 128) <= 256
+               ? launch_tile<128, 128, 2, 2, 2, 1, false, false>(a, st)
+               : launch_tile<64, 128, 2, 2, 2, 1, false, false>(a, st);
   }
   switch (dense_plan(a.m, a.n, a.k).way) {
     case kStreamed:
