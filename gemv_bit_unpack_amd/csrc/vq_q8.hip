@@ -494,23 +494,21 @@ __global__ __launch_bounds__(256) void q8_join_kernel(Q8Args a) {
 // ---------------------------------------------------------------- few rows
 
 // Few tokens: the weights are read once, straight into the matrix instruction's registers.  A workgroup of 8 wavefronts
-// takes WN x RT blocks of 16 weight rows and up to 16 MT tokens; the WK = 8 / WN wavefronts of a row block cut K, their
-// int32 sums meet in LDS.  Bound by the weights' bytes and, with small matrices, by the latency of one pass over K:
-// 2 x 14336 x 4096 takes 16.5 us (3.6 TB/s), 16 x 4096 x 4096 7.5 us.
-template <int RT, int MT, int WN>
+// takes RT blocks of 16 weight rows and up to 16 MT tokens; its wavefronts cut K, their int32 sums meet in LDS.  Bound by
+// the weights' bytes (8 x 8192 x 8192: 17.9 us, 3.8 TB/s) and, with small matrices, by the latency of one pass over K
+// (16 x 4096 x 4096: 7.1 us).
+template <int RT, int MT>
 __global__ __launch_bounds__(512) void q8_few_kernel(Q8Args a) {
-  constexpr int WK = 8 / WN;
   constexpr int kTiles = RT * MT;
-  constexpr int U = RT * MT == 1 ? 8 : RT * MT <= 6 ? 4 : 2;  // 64-byte steps in flight
+  constexpr int U = RT * MT == 1 ? 8 : 4;  // 64-byte steps in flight
   __shared__ v4i red[8][kTiles][64];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wk = wave % WK, wn = wave / WK;
-  const int32_t n0 = ((int32_t)blockIdx.x * WN + wn) * 16 * RT;
+  const int32_t n0 = (int32_t)blockIdx.x * 16 * RT;
   const int64_t ld = vqi::q8_row_bytes(a.k);
   const int32_t steps = (int32_t)(ld / 64);
-  const int32_t k0 = steps * wk / WK, k1 = steps * (wk + 1) / WK;
+  const int32_t k0 = steps * wave / 8, k1 = steps * (wave + 1) / 8;
   const int row = lane & 15, grp = lane >> 4;
 
   const uint8_t* gw[RT];
@@ -571,14 +569,14 @@ __global__ __launch_bounds__(512) void q8_few_kernel(Q8Args a) {
     for (int j = 0; j < MT; ++j) red[wave][i * MT + j][lane] = acc[i][j];
   __syncthreads();
 
-  // lane: token lane % 16, channels 4 (lane / 16) .. + 3 of a block; the WK wavefronts share the blocks out
-  for (int o = wk; o < kTiles; o += WK) {
+  // lane: token lane % 16, channels 4 (lane / 16) .. + 3 of a block; the wavefronts share the blocks out
+  for (int o = wave; o < kTiles; o += 8) {
     const int j = o % MT, i = o / MT;
     const int32_t m = 16 * j + row;
     const int32_t n = n0 + 16 * i + 4 * grp;
-    v4i sum = red[wn * WK][o][lane];
+    v4i sum = red[0][o][lane];
 #pragma unroll
-    for (int v = 1; v < WK; ++v) sum += red[wn * WK + v][o][lane];
+    for (int v = 1; v < 8; ++v) sum += red[v][o][lane];
     if (m >= a.m) continue;
     const float s = a.s[m];
     float sc[4], b[4], v[4];
@@ -838,20 +836,12 @@ __global__ __launch_bounds__(512) void q8_one_kernel(OneArgs a) {
 // One token, 14336 x 4096: 15.9 us with 64 rows, 16.9 with 32 and 18.1 with 16; 4096 x 4096: 13.9, 9.2 and 8.4 us.
 inline int rows_per_group(int32_t n) { return n / 64 >= 192 ? 64 : n / 32 > 144 ? 32 : 16; }
 
-template <int RT, int MT, int WN>
+template <int RT, int MT>
 vq_status launch_few(const Q8Args& a, hipStream_t st) {
-  const int64_t blocks = ((int64_t)a.n + WN * RT * 16 - 1) / (WN * RT * 16);
+  const int64_t blocks = ((int64_t)a.n + RT * 16 - 1) / (RT * 16);
   if (!vqi::grid_ok(blocks, 512)) return VQ_ERR_SHAPE;
-  q8_few_kernel<RT, MT, WN><<<dim3((uint32_t)blocks), dim3(512), 0, st>>>(a);
+  q8_few_kernel<RT, MT><<<dim3((uint32_t)blocks), dim3(512), 0, st>>>(a);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
-}
-template <int MT>
-vq_status launch_few_rows(const Q8Args& a, hipStream_t st) {
-  switch (rows_per_group(a.n)) {
-    case 64: return launch_few<2, MT, 2>(a, st);
-    case 32: return launch_few<2, MT, 1>(a, st);
-    default: return launch_few<1, MT, 1>(a, st);
-  }
 }
 
 template <int BM, int BN, int WM, int WN, int NB, int KG, bool GATED, bool SPLIT>
@@ -926,14 +916,32 @@ struct Plan {
   Way way;
   int32_t splits;  // cuts of K over the CUs
 };
+// Few rows are streamed as long as that costs less than the tiles' fixed part, several steps of a microsecond.  It grows
+// with what the busiest CU does: its blocks of 16 weight rows, times the steps of K, times the weights and each block of
+// 16 tokens.  us, streamed and in tiles, weights from memory:
+//   one block, tokens x steps: 1030 x 777, 64 rows 4.9 and 5.2; 2500 x 2048, 32 rows 5.6 and 6.2, 48 rows 6.7 and 6.3;
+//     4096 x 4096, 32 rows 8.4 and 9.4, 48 rows 10.4 and 10.0; 1030 x 5120, 16 rows 8.6 and 10.2, 32 rows 11.0 and 10.0
+//   two: 4500 x 777, 32 rows 5.6 and 5.5, 48 rows 6.7 and 5.4; 7000 x 2048, 16 rows 6.2 and 7.6; 6144 x 4096, 16 rows
+//     9.5 and 9.4; 7000 x 5120, 16 rows 14.5 and 11.7; where all CUs are at work 8192 x 8192, 2 rows 17.1 and 19.5, 8 rows
+//     17.9 and 19.5, 16 rows 19.2 and 19.5 (7300 x 5120, 2 rows 14.3 and 12.5: steps left over from blocks of four)
+//   four: 9000 x 2048, 2 rows 8.2 and 8.8, 16 rows 9.2 and 8.6; 11008 x 4096, 2 rows 15.2 and 14.7, 16 rows 16.9 and
+//     13.5; wider ones: 14336 x 2048, 2 rows 9.6 and 9.2; 28672 x 8192, 16 rows 62 and 48
+//   few columns with a long K, which the tiles cut over the CUs: 256 x 8192, 2 rows 8.0 and 7.0
+bool streamed(int32_t m, int32_t n, int64_t steps) {
+  if (m > 64 || (n < 1024 && steps >= 56)) return false;
+  const int32_t tokens = (m + 15) / 16;
+  const int32_t wide = rows_per_group(n);
+  const int64_t groups = ((int64_t)n + wide - 1) / wide;
+  const int64_t blocks = (groups + 255) / 256 * (wide / 16);
+  if (blocks == 1) return tokens * steps <= 64 && (tokens <= 2 || steps <= 8);
+  if (blocks == 2)
+    return (tokens == 1 && steps <= 32) || (tokens == 2 && steps <= 8) || (m <= 8 && steps <= 64 && groups > 224);
+  return wide == 32 && m <= 8 && steps <= 16;
+}
+
 Plan dense_plan(int32_t m, int32_t n, int32_t k) {
-  // us, streamed and in the tiles that would be taken: 4096 x 4096, 16 rows 7.5 and 9.0, 48 rows 10.7 and 9.0;
-  // 5003 x 4099, 16 rows 11.2 and 10.2; 8192 x 8192, 16 rows 17.0 and 20.5; 4096 x 14336, 16 rows 20.0 and 17.2
-  // (40 x 64 x 65536, four workgroups: 104 us streamed)
-  const int64_t nk = (int64_t)n * k;
   const int64_t steps = q8_row_bytes(k) / kStep;
-  if (m <= 64 && (n >= 1024 || steps < 56) && (m * nk <= 400000000 || (m <= 16 && k <= 8192 && nk <= 70000000)))
-    return {kStreamed, 1};
+  if (streamed(m, n, steps)) return {kStreamed, 1};
   auto tiles = [&](int bm, int bn) { return (((int64_t)m + bm - 1) / bm) * (((int64_t)n + bn - 1) / bn); };
   // K is cut where the tiles leave CUs without work, if it is long enough to pay for the second launch (the int32 partial
   // sums), and then over as many CUs as find 8 steps each
@@ -988,10 +996,11 @@ vq_status launch_q8(const Q8Args& a, void* stream) {
                : launch_tile<64, 128, 2, 2, 2, 1, false, false>(a, st);
   }
   switch (dense_plan(a.m, a.n, a.k).way) {
-    case kStreamed:
-      if (a.m <= 16) return launch_few_rows<1>(a, st);
-      if (a.m <= 32) return launch_few_rows<2>(a, st);
-      return a.m <= 48 ? launch_few_rows<3>(a, st) : launch_few_rows<4>(a, st);
+    case kStreamed:  // groups of 32 weight rows take 32 tokens at most, 64 none (streamed)
+      if (rows_per_group(a.n) > 16) return a.m <= 16 ? launch_few<2, 1>(a, st) : launch_few<2, 2>(a, st);
+      if (a.m <= 16) return launch_few<1, 1>(a, st);
+      if (a.m <= 32) return launch_few<1, 2>(a, st);
+      return a.m <= 48 ? launch_few<1, 3>(a, st) : launch_few<1, 4>(a, st);
     case k64x32: return launch_tile<64, 32, 2, 1, 4, 2, false, false>(a, st);
     case k64x64: {
       if (a.splits == 1) return launch_tile<64, 64, 2, 2, 4, 1, false, false>(a, st);
