@@ -126,9 +126,11 @@ vq_status launch_expert_plan(int32_t tokens, int32_t top, int32_t experts, const
 }
 
 vq_status launch_expert_combine(int32_t tokens, int32_t top, int32_t n, int32_t rows, const float* z,
-                                const int32_t* pos, const float* p, void* y, vq_dtype y_dtype, void* stream) {
+                                const int32_t* pos, const float* p, void* y, vq_dtype y_dtype, void* stream,
+                                bool check_only) {
   const int64_t items = (int64_t)tokens * ((n + 3) / 4);
   if (!vqi::grid_ok((items + 255) / 256, 256)) return VQ_ERR_SHAPE;
+  if (check_only) return VQ_OK;
   expert_combine_kernel<<<dim3((uint32_t)((items + 255) / 256)), dim3(256), 0, (hipStream_t)stream>>>(
       tokens, top, n, rows, z, pos, p, y, y_dtype);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;

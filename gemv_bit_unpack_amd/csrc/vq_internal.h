@@ -141,6 +141,8 @@ vq_status launch_assign(const vq_desc& d, const void* w, vq_dtype w_dtype, const
                         uint32_t* idx1, uint32_t* idx2, void* workspace, void* stream);
 
 // ---- 8-bit operators (vq_q8_*, vq_expert_*, vq_block_norm) ----
+// `check_only`: whether the launch would be made (VQ_ERR_SHAPE: its grid is too large), for calls of several launches that
+// have to refuse before the first (of the products the grouped one).
 
 // Whether a launch of `blocks` workgroups of `threads` stays inside the 32-bit grid.
 inline bool grid_ok(int64_t blocks, int64_t threads) { return blocks >= 1 && blocks * threads <= 0xFFFFFFFFll; }
@@ -175,7 +177,7 @@ struct NormArgs {
   uint8_t* q;  // [rows][q8_row_bytes(dim)] or nullptr
   float* s;    // [rows]
 };
-vq_status launch_norm(const NormArgs& a, void* stream);
+vq_status launch_norm(const NormArgs& a, void* stream, bool check_only = false);
 
 // An 8-bit product, dense (experts == 0) or grouped by expert (validated arguments; vq_q8.hip).
 struct Q8Args {
@@ -199,7 +201,7 @@ struct Q8Args {
 };
 // K splits that a dense product of this shape uses; its workspace is splits * m * n int32 where splits > 1.
 int32_t q8_splits(int32_t m, int32_t n, int32_t k);
-vq_status launch_q8(const Q8Args& a, void* stream);
+vq_status launch_q8(const Q8Args& a, void* stream, bool check_only = false);
 
 // Products of one token that is cut to 8 bits inside the kernel (vq_q8.hip): dense (experts == 0), the gated products of
 // its `slots` experts (y fp32 [slots][n], x one row), or their joined outputs (join: x fp32 [slots][k], y [n]).
@@ -234,6 +236,7 @@ vq_status launch_q8_one(const OneArgs& a, void* stream);
 vq_status launch_expert_plan(int32_t tokens, int32_t top, int32_t experts, const int32_t* ids, int32_t* offsets,
                              int32_t* rows, int32_t* pos, void* stream);
 vq_status launch_expert_combine(int32_t tokens, int32_t top, int32_t n, int32_t rows, const float* z,
-                                const int32_t* pos, const float* p, void* y, vq_dtype y_dtype, void* stream);
+                                const int32_t* pos, const float* p, void* y, vq_dtype y_dtype, void* stream,
+                                bool check_only = false);
 
 }  // namespace vqi

@@ -349,12 +349,13 @@ __global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs a) {
 }
 
 template <int C, bool ONE, int MAXT, bool AHEAD>
-vq_status launch(const NormArgs& a, hipStream_t stream) {
+vq_status launch(const NormArgs& a, hipStream_t stream, bool check_only) {
   // whole 128-byte steps of q have to be covered, pad included: 16 chunks
   const int chunks = (int)(vqi::q8_row_bytes(a.dim) / kChunk);
   const int wg = ONE ? 256 : ((chunks + C - 1) / C + 63) / 64 * 64;
   const int64_t blocks = ONE ? ((int64_t)a.rows + 3) / 4 : a.rows;
   if (!vqi::grid_ok(blocks, wg)) return VQ_ERR_SHAPE;
+  if (check_only) return VQ_OK;
   const dim3 g((uint32_t)blocks), b(wg);
   if (a.z_dtype == VQ_F32) {
     if (a.h_dtype == VQ_F32) norm_kernel<C, ONE, MAXT, AHEAD, true, true><<<g, b, 0, stream>>>(a);
@@ -373,19 +374,19 @@ constexpr int kFewRows = 512;
 
 namespace vqi {
 
-vq_status launch_norm(const NormArgs& a, void* stream_) {
+vq_status launch_norm(const NormArgs& a, void* stream_, bool check_only) {
   hipStream_t stream = (hipStream_t)stream_;
   const int d = a.dim;
-  if (d <= 512) return launch<1, true, 256, true>(a, stream);
+  if (d <= 512) return launch<1, true, 256, true>(a, stream, check_only);
   // measured, 8192-wide rows with both norms, gate and residual in bf16: 64 rows 6.7 us with one chunk per thread and
   // 7.4 us with two; 8192 rows 181 us and 140 us
   if (a.rows > kFewRows || d > 8192) {
-    if (d <= 8192) return launch<2, false, 512, false>(a, stream);
-    if (d <= 16384) return launch<2, false, 1024, false>(a, stream);
-    if (d <= 32768) return launch<4, false, 1024, false>(a, stream);
-    return launch<8, false, 1024, false>(a, stream);  // up to kNormMaxDim
+    if (d <= 8192) return launch<2, false, 512, false>(a, stream, check_only);
+    if (d <= 16384) return launch<2, false, 1024, false>(a, stream, check_only);
+    if (d <= 32768) return launch<4, false, 1024, false>(a, stream, check_only);
+    return launch<8, false, 1024, false>(a, stream, check_only);  // up to kNormMaxDim
   }
-  return launch<1, false, 1024, true>(a, stream);
+  return launch<1, false, 1024, true>(a, stream, check_only);
 }
 
 }  // namespace vqi

@@ -845,12 +845,13 @@ vq_status launch_few(const Q8Args& a, hipStream_t st) {
 }
 
 template <int BM, int BN, int WM, int WN, int NB, int KG, bool GATED, bool SPLIT>
-vq_status launch_tile(const Q8Args& a, hipStream_t st) {
+vq_status launch_tile(const Q8Args& a, hipStream_t st, bool check_only = false) {
   const int out = GATED ? BN / 2 : BN;
   const int64_t mt = a.experts ? span_bound(a, BM) : ((int64_t)a.m + BM - 1) / BM;
   const int64_t nt = ((int64_t)a.n + out - 1) / out;
   constexpr int kThreads = 64 * WM * WN * KG;
   if (!vqi::grid_ok(mt * nt + 8, kThreads)) return VQ_ERR_SHAPE;
+  if (check_only) return VQ_OK;
   const uint32_t blocks = (uint32_t)((mt * nt + 7) / 8 * 8);
   q8_tile_kernel<BM, BN, WM, WN, NB, KG, GATED, SPLIT>
       <<<dim3(blocks, SPLIT ? a.splits : 1), dim3(kThreads), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
@@ -862,12 +863,13 @@ vq_status launch_join(const Q8Args& a, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
 }
 template <bool GATED>
-vq_status launch_big(const Q8Args& a, hipStream_t st) {
+vq_status launch_big(const Q8Args& a, hipStream_t st, bool check_only = false) {
   const int out = GATED ? 128 : 256;
   const int64_t mt = a.experts ? span_bound(a, 256) : ((int64_t)a.m + 255) / 256;
   const int64_t nt = ((int64_t)a.n + out - 1) / out;
   const int64_t blocks = mt * nt + 128 + 8;  // at most 128 tiles are cut in two
   if (!vqi::grid_ok(blocks, 512)) return VQ_ERR_SHAPE;
+  if (check_only) return VQ_OK;
   q8_big_kernel<GATED><<<dim3((uint32_t)blocks), dim3(512), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
   return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
 }
@@ -971,7 +973,7 @@ Plan dense_plan(int32_t m, int32_t n, int32_t k) {
 
 int32_t q8_splits(int32_t m, int32_t n, int32_t k) { return dense_plan(m, n, k).splits; }
 
-vq_status launch_q8(const Q8Args& a, void* stream) {
+vq_status launch_q8(const Q8Args& a, void* stream, bool check_only) {  // check_only: the grouped product
   hipStream_t st = (hipStream_t)stream;
   if (a.experts) {
     // Rows of a group on average (in the larger of max_rows' bound): short groups take small tiles, in between the plain
@@ -986,14 +988,15 @@ vq_status launch_q8(const Q8Args& a, void* stream) {
     const int64_t groups = a.m < a.experts ? a.m : a.experts;
     const int64_t avg = (a.m + groups - 1) / groups;
     if (a.gated) {
-      if (avg <= 4) return launch_tile<32, 128, 1, 2, 2, 1, true, false>(a, st);
-      return avg <= 96 ? launch_tile<64, 128, 2, 2, 2, 1, true, false>(a, st) : launch_big<true>(a, st);
+      if (avg <= 4) return launch_tile<32, 128, 1, 2, 2, 1, true, false>(a, st, check_only);
+      return avg <= 96 ? launch_tile<64, 128, 2, 2, 2, 1, true, false>(a, st, check_only)
+                       : launch_big<true>(a, st, check_only);
     }
-    if (avg <= 48) return launch_tile<32, 128, 1, 4, 2, 1, false, false>(a, st);
-    if (avg > 192) return launch_big<false>(a, st);
+    if (avg <= 48) return launch_tile<32, 128, 1, 4, 2, 1, false, false>(a, st, check_only);
+    if (avg > 192) return launch_big<false>(a, st, check_only);
     return (avg + 127) / 128 * groups * (((int64_t)a.n + 127) / 128) <= 256
-               ? launch_tile<128, 128, 2, 2, 2, 1, false, false>(a, st)
-               : launch_tile<64, 128, 2, 2, 2, 1, false, false>(a, st);
+               ? launch_tile<128, 128, 2, 2, 2, 1, false, false>(a, st, check_only)
+               : launch_tile<64, 128, 2, 2, 2, 1, false, false>(a, st, check_only);
   }
   switch (dense_plan(a.m, a.n, a.k).way) {
     case kStreamed:  // groups of 32 weight rows take 32 tokens at most, 64 none (streamed)

@@ -79,7 +79,7 @@ vq_status check_routing(int32_t tokens, int32_t top, int32_t experts) {
 }
 
 vq_status quantize(int32_t rows, int32_t k, const void* x, vq_dtype t, int64_t ldx, uint8_t* q, float* s,
-                   void* stream) {
+                   void* stream, bool check_only = false) {
   NormArgs a;
   std::memset(&a, 0, sizeof a);
   a.rows = rows;
@@ -90,7 +90,41 @@ vq_status quantize(int32_t rows, int32_t k, const void* x, vq_dtype t, int64_t l
   a.gate_rows = 1;
   a.q = q;
   a.s = s;
-  return launch_norm(a, stream);
+  return launch_norm(a, stream, check_only);
+}
+
+vq_status grouped(int32_t experts, int32_t max_rows, int32_t tokens, int32_t N, int32_t K, const int32_t* offsets,
+                  const int32_t* rows, const void* q, const float* s, const void* w, const float* sw, const void* bias,
+                  int32_t gated, void* y, vq_dtype y_dtype, void* stream, bool check_only = false) {
+  if (experts < 1 || experts > kMaxExperts || max_rows < 0 || max_rows >= kMaxPairs || tokens < 0 || N < 0 ||
+      N > INT32_MAX / 2 || !valid_k(K))
+    return VQ_ERR_SHAPE;
+  if (!valid_dtype(y_dtype) || (gated != 0 && gated != 1)) return VQ_ERR_UNSUPPORTED;
+  if (max_rows == 0 || N == 0) return VQ_OK;
+  if (tokens < (rows ? 1 : max_rows)) return VQ_ERR_SHAPE;
+  if (!offsets || !q || !s || !w || !sw || !y) return VQ_ERR_NULL;
+  if (!aligned(offsets, 4) || misaligned(rows, 4) || !aligned(q, 16) || !aligned(w, 16) || !aligned(s, 4) ||
+      !aligned(sw, 4) || misaligned(bias, 2) || !aligned(y, size_of(y_dtype)))
+    return VQ_ERR_ALIGN;
+  Q8Args a;
+  std::memset(&a, 0, sizeof a);
+  a.m = max_rows;
+  a.tokens = tokens;
+  a.n = N;
+  a.k = K;
+  a.q = (const uint8_t*)q;
+  a.s = s;
+  a.w = (const uint8_t*)w;
+  a.sw = sw;
+  a.bias = (const uint16_t*)bias;
+  a.y = y;
+  a.y_dtype = y_dtype;
+  a.experts = experts;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.gated = gated;
+  a.splits = 1;
+  return launch_q8(a, stream, check_only);
 }
 
 }  // namespace
@@ -207,35 +241,7 @@ vq_status vq_q8_gemm_grouped(int32_t experts, int32_t max_rows, int32_t tokens, 
                              const int32_t* offsets, const int32_t* rows, const void* q, const float* s, const void* w,
                              const float* sw, const void* bias, int32_t gated, void* y, vq_dtype y_dtype,
                              void* stream) {
-  if (experts < 1 || experts > kMaxExperts || max_rows < 0 || max_rows >= kMaxPairs || tokens < 0 || N < 0 ||
-      N > INT32_MAX / 2 || !valid_k(K))
-    return VQ_ERR_SHAPE;
-  if (!valid_dtype(y_dtype) || (gated != 0 && gated != 1)) return VQ_ERR_UNSUPPORTED;
-  if (max_rows == 0 || N == 0) return VQ_OK;
-  if (tokens < (rows ? 1 : max_rows)) return VQ_ERR_SHAPE;
-  if (!offsets || !q || !s || !w || !sw || !y) return VQ_ERR_NULL;
-  if (!aligned(offsets, 4) || misaligned(rows, 4) || !aligned(q, 16) || !aligned(w, 16) || !aligned(s, 4) ||
-      !aligned(sw, 4) || misaligned(bias, 2) || !aligned(y, size_of(y_dtype)))
-    return VQ_ERR_ALIGN;
-  Q8Args a;
-  std::memset(&a, 0, sizeof a);
-  a.m = max_rows;
-  a.tokens = tokens;
-  a.n = N;
-  a.k = K;
-  a.q = (const uint8_t*)q;
-  a.s = s;
-  a.w = (const uint8_t*)w;
-  a.sw = sw;
-  a.bias = (const uint16_t*)bias;
-  a.y = y;
-  a.y_dtype = y_dtype;
-  a.experts = experts;
-  a.offsets = offsets;
-  a.rows = rows;
-  a.gated = gated;
-  a.splits = 1;
-  return launch_q8(a, stream);
+  return grouped(experts, max_rows, tokens, N, K, offsets, rows, q, s, w, sw, bias, gated, y, y_dtype, stream);
 }
 
 vq_status vq_expert_combine(int32_t tokens, int32_t top, int32_t N, int32_t max_rows, const float* z,
@@ -306,16 +312,22 @@ vq_status vq_q8_experts(int32_t tokens, int32_t top, int32_t experts, int32_t D,
       return launch_q8_one(out, stream);
     }
   }
-  if ((st = launch_expert_plan(tokens, top, experts, ids, ws.offsets, ws.rows, ws.pos, stream)) != VQ_OK) return st;
-  if ((st = quantize(tokens, D, x, x_dtype, ldx, ws.xq, ws.xs, stream)) != VQ_OK) return st;
-  if ((st = vq_q8_gemm_grouped(experts, pairs, tokens, I, D, ws.offsets, ws.rows, ws.xq, ws.xs, w_in, s_in, nullptr, 1,
-                               ws.h, VQ_F32, stream)) != VQ_OK)
-    return st;
-  if ((st = quantize(pairs, I, ws.h, VQ_F32, I, ws.hq, ws.hs, stream)) != VQ_OK) return st;
-  if ((st = vq_q8_gemm_grouped(experts, pairs, pairs, D, I, ws.offsets, nullptr, ws.hq, ws.hs, w_out, s_out, nullptr, 0,
-                               ws.z, VQ_F32, stream)) != VQ_OK)
-    return st;
-  return launch_expert_combine(tokens, top, D, pairs, ws.z, ws.pos, p, y, y_dtype, stream);
+  auto run = [&](bool check_only) {
+    if (!check_only &&
+        (st = launch_expert_plan(tokens, top, experts, ids, ws.offsets, ws.rows, ws.pos, stream)) != VQ_OK)
+      return st;
+    if ((st = quantize(tokens, D, x, x_dtype, ldx, ws.xq, ws.xs, stream, check_only)) != VQ_OK) return st;
+    if ((st = grouped(experts, pairs, tokens, I, D, ws.offsets, ws.rows, ws.xq, ws.xs, w_in, s_in, nullptr, 1, ws.h,
+                      VQ_F32, stream, check_only)) != VQ_OK)
+      return st;
+    if ((st = quantize(pairs, I, ws.h, VQ_F32, I, ws.hq, ws.hs, stream, check_only)) != VQ_OK) return st;
+    if ((st = grouped(experts, pairs, pairs, D, I, ws.offsets, nullptr, ws.hq, ws.hs, w_out, s_out, nullptr, 0, ws.z,
+                      VQ_F32, stream, check_only)) != VQ_OK)
+      return st;
+    return launch_expert_combine(tokens, top, D, pairs, ws.z, ws.pos, p, y, y_dtype, stream, check_only);
+  };
+  if ((st = run(true)) != VQ_OK) return st;
+  return run(false);
 }
 
 vq_status vq_block_norm(const vq_norm_desc* desc, const void* z, const void* h, const void* post_w, const void* post_b,

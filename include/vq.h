@@ -383,7 +383,8 @@ vq_status vq_assign(const vq_desc* desc, const void* w, vq_dtype w_dtype, const 
 /*
  * 8-bit operators: what a block with some layers kept in 8 bits runs next to its codebook
  * layers.  Everything above on ownership, streams and errors holds for them: device
- * pointers, the caller's stream and workspace, arguments checked before any launch.
+ * pointers, the caller's stream and workspace, arguments checked before any launch (rows
+ * that would need a grid of 2^32 threads or more among them: VQ_ERR_SHAPE).
  *
  * An 8-bit matrix of k columns is stored in rows of vq_q8_row_bytes(k) = 128 ceil(k / 128)
  * bytes, one int8 per column, the pad bytes ZERO (vq_q8_quantize and vq_block_norm write
