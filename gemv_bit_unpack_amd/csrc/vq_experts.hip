@@ -9,7 +9,9 @@ namespace {
 // first sorted row) and those equal to e, each thread over a contiguous share of the pairs; a prefix sum over the
 // threads gives every thread its first row, and the second sweep writes.  The pairs of an expert keep their order, so
 // the plan does not depend on timing.  The id list is read E times from the caches (the first 8 of a thread's share stay in
-// registers between the sweeps): 8192 pairs over 8 experts take 9 us, 1332 over 64 take 4.6, most of it latency.
+// registers between the sweeps): 8192 pairs over 8 experts take 9 us, 1332 over 64 take 4.6, most of it latency.  Past
+// 8192 pairs each thread reads the rest of its share one id after the other, twice: 32768 pairs over 128 experts take 39 us,
+// 262144 over 64 take 258, about 1 us for each id of a share.
 constexpr int kThreads = 1024;
 constexpr int kHeld = 8;
 

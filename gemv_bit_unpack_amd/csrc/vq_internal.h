@@ -149,8 +149,8 @@ inline bool grid_ok(int64_t blocks, int64_t threads) { return blocks >= 1 && blo
 
 // Bytes of one row of an 8-bit matrix of k columns: whole 128-byte matrix steps, the pad zero.
 constexpr int64_t q8_row_bytes(int64_t k) { return (k + 127) / 128 * 128; }
-// Largest K of the products and longest row of the row pass, which holds a row in the registers of one workgroup.  (An
-// int32 sum would hold 131071 products of magnitude 128 * 128.)
+// Largest K of the products and longest row of the row pass, which one workgroup holds.  (An int32 sum would hold 131071
+// products of magnitude 128 * 128.)
 constexpr int32_t kQ8MaxK = 65536;
 constexpr int32_t kNormMaxDim = 65536;
 

@@ -8,10 +8,14 @@
 // with N(a) = (a - mean) / sqrt(mean((a - mean)^2) + eps) * (w_offset + w) + b; the RMS form has no mean, "none" is the
 // identity.  The quantizer alone is the same kernel with z = x and both norms off.
 //
-// A row is held in registers from its one load to its one store, fp32 from the first widening on: C chunks of 8
+// A row is held by its threads from its one load to its one store, fp32 from the first widening on: C chunks of 8
 // elements per thread (chunk c of thread t is elements 8 (c T + t) .. for T threads), so the statistics of both norms,
 // the residual add and the row's largest value cost no second read, and everything is rounded once, at the store.  The
 // variance is taken about the mean in a second sweep over the registers: no cancellation.
+// Up to 32768 elements the registers hold it.  Longer rows, 8 chunks for each of 1024 threads, need more than the 128
+// registers that these have: the compiler keeps 180 to 356 bytes a thread in scratch memory, and a row costs four times
+// as much as one half as long (both norms, gate and residual in bf16: 16 x 65536 68 us, 16 x 32768 15; 1024 rows 391 and
+// 86; the quantizer alone, fp32, 1024 rows 108 and 43).
 //
 // Bound: the bytes of z, h, r and x once each; 8192 x 8192 in bf16 with everything on, 537 MB, takes 140 us (3.8 TB/s;
 // the vector instructions, about 20 per element, are half of that).  With few rows time is the chain load - sum - sum -
@@ -384,7 +388,7 @@ vq_status launch_norm(const NormArgs& a, void* stream_, bool check_only) {
     if (d <= 8192) return launch<2, false, 512, false>(a, stream, check_only);
     if (d <= 16384) return launch<2, false, 1024, false>(a, stream, check_only);
     if (d <= 32768) return launch<4, false, 1024, false>(a, stream, check_only);
-    return launch<8, false, 1024, false>(a, stream, check_only);  // up to kNormMaxDim
+    return launch<8, false, 1024, false>(a, stream, check_only);  // up to kNormMaxDim, partly in scratch
   }
   return launch<1, false, 1024, true>(a, stream, check_only);
 }

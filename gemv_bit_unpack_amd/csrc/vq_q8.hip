@@ -145,7 +145,7 @@ __device__ __forceinline__ void to_lds(const uint8_t* g, uint8_t* l) {
 
 // The workgroup's barrier alone.  __syncthreads() would also wait for every load to LDS that is still on its way; here
 // each wavefront has waited for those that the others need, and for its own reads, and no memory operation moves across.
-// 64 x 8192 x 8192 in 64 x 128 tiles of three steps: 53 us with __syncthreads(), 34 us.
+// 64 x 8192 x 8192 (64 x 32 tiles): 30 us with __syncthreads(), 21 us; 128 x 28672 x 8192 (128 x 128): 72 and 58 us.
 __device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
@@ -604,7 +604,8 @@ template <int RT, int WN, bool GATED, bool JOIN, vq_dtype XT>
 __global__ __launch_bounds__(512) void q8_one_kernel(OneArgs a) {
   constexpr int WK = 8 / WN;
   // 64-byte steps of a block (JOIN: 14336 columns are 28 steps per wavefront, whole blocks of 4: 30.6 us for 2 experts
-  // of 4096 rows, 31.8 with blocks of 8 and 4 steps left over)
+  // of 4096 rows, 31.8 with blocks of 8 and 4 steps left over).  Steps left over are loaded one by one: with 10 steps per
+  // wavefront 5120 x 5120 takes 13.8 us, with 8 4096 x 4096 takes 7.5, each with its weights from memory
   constexpr int U = RT == 1 && !JOIN ? 8 : 4;
   constexpr int kOut = GATED ? 16 : 16 * RT;
   static_assert(!GATED || RT == 2, "one gate block and one up block");
@@ -951,21 +952,25 @@ Plan dense_plan(int32_t m, int32_t n, int32_t k) {
     return steps < 56 ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / t, steps / 8));
   };
   const int64_t narrow = tiles(64, 32), small = tiles(64, 64), tall = tiles(128, 64), wide = tiles(128, 128);
-  // 512 x 28672 x 8192 (224 of them): 117 us against 156 in 128 x 128; 1024 x 8192 x 8192 (128): 100 against 73
+  // All us below: one run, weights from memory, / 4 for a K cut in 4 (with the join).
+  // 512 x 28672 x 8192 (224 tiles): 122 against 154 in 128 x 128; 2048 x 8192 x 2048 (256): 38 and 47; 1024 x 8192 x 8192
+  // (128): 87 and 78; 1500 x 4096 x 4096 (96): 40 and 36
   if (tiles(256, 256) >= 200) return {k256x256, 1};
-  // at most one for each CU, with two groups of wavefronts that halve K: 37 x 5003 x 4099 10.2 us (64 x 64: 12.8),
-  // 128 x 4096 x 4096 9.4 (12.0), 64 x 8192 x 8192 20.5 (22.5 cut in 4); 256 x 4096 x 4096, 512 of them, 16.4 (12.5);
-  // 64 x 4096 x 14336, 128 of them, 29.3 (20.3 cut in 4); 64 x 8192 x 28672 68 (53 cut in 2)
+  // at most one for each CU, with two groups of wavefronts that halve K, against 64 x 64: 37 x 5003 x 4099 10.7 and 12.4 / 3,
+  // 128 x 4096 x 4096 10.7 and 12.8, 200 x 2000 x 3000 8.4 and 9.9, 64 x 8192 x 8192 23.0 and 23.2 / 2; 300 x 2500 x 2500
+  // (395 of them) 13.1 and 9.5; longer K: 64 x 4096 x 14336 29 and 20 / 4, 64 x 8192 x 28672 64 and 53 / 2
   if (narrow <= 256 && steps < (narrow > 128 ? 100 : 56)) return {k64x32, 1};
-  // 64 x 28672 x 8192: 53 us; 256 x 4096 x 4096: 12.5 against 15.1 in 128 x 64 and 23 in 128 x 128; 64 x 4096 x 14336:
-  // 19.4 cut in 4, 37 uncut.  128 x 8192 x 28672, where each step counts: 82 us against 63 in 128 x 128 cut in 4
+  // 256 x 4096 x 4096: 13.1 against 17.5 in 128 x 64 and 21 / 4 in 128 x 128; 64 x 4096 x 14336: 20.0 / 4, 37 uncut;
+  // longer K: 128 x 8192 x 28672 78 against 61 / 4 in 128 x 128
   if (m <= 64 || (small <= 256 && steps < (small > 128 ? 100 : 128))) return {k64x64, cut(small)};
-  // 128 x 14336 x 4096: 20.8 us against 23.8 in 64 x 64 and 26.2 in 128 x 128; 256 x 8192 x 8192: 33.7, 41.4 and 37.8
+  // against 64 x 64 and 128 x 128: 128 x 14336 x 4096 20.6, 23.7 and 25 / 2; 256 x 8192 x 8192 33.5, 38.5 and 35 / 2;
+  // 512 x 4096 x 4096 17.6, 19.3 and 22.5; more than one round: 300 x 6500 x 2048 (306 tiles) 13.8, 10.9 and 14.9
   if (tall >= 160 && tall <= 256 && steps < 128) return {k128x64, 1};
-  // 512 x 4096 x 4096: 17.0 us against 22.4 in 128 x 128
+  // against 128 x 128: 320 x 6500 x 3000 17.9 and 19.1; 300 x 6500 x 4900 (39 steps) 25.3 and 25.6; 400 x 5000 x 5120 (40)
+  // 33.2 and 27.0.  With few rows 128 x 64 would be nearer: 128 x 9300 x 3000 19.1, 17.0 there
   if (small <= 512 && steps < 40) return {k64x64, 1};
-  // one workgroup per CU and three steps in LDS, or two workgroups and two steps: 128 x 28672 x 8192 (224 tiles) 60.7
-  // and 71.6 us, 512 x 14336 x 4096 (448) 49.5 and 44.1
+  // one workgroup per CU and three steps in LDS, or two workgroups and two steps: 128 x 28672 x 8192 (224 tiles) 60.5
+  // and 66.2; 700 x 7000 x 3000 (330) 36.6 and 29.0; 512 x 14336 x 4096 (448) 48.5 and 42.8
   if (wide <= 256) return {k128x128, cut(wide)};
   return {k128x128Pair, 1};
 }
