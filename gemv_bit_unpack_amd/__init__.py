@@ -20,7 +20,8 @@ device buffers for gemv_ws / gemm_ws, and ``VQLinear``, a layer object holding t
 weights that picks gemv_ws or gemm_ws by batch size, the analogue of the VPTQ guide's
 ``VPTQLinear`` module.  The 8-bit operators (layers kept in 8 bits, their experts, the norms
 between blocks) are in ``q8`` and re-exported here: q8_*, expert_*, block_norm, Q8Linear,
-Q8Experts.
+Q8Experts; so are the layers in 8-bit floats of ``f8`` (f8_*, F8Linear, F8MLP) and the heads'
+norms and rotary positions of ``heads`` (rope_frequencies, Rotary, rotate_heads).
 """
 from __future__ import annotations
 
@@ -53,7 +54,9 @@ EXPORTED = ("vq_abi_version", "vq_status_string", "vq_packed_bytes", "vq_pack", 
             "vq_gemm_workspace_bytes", "vq_gemm_ws", "vq_rht_product_workspace_bytes", "vq_gemv_ws_rht",
             "vq_gemm_ws_rht", "vq_q8_row_bytes", "vq_q8_quantize", "vq_q8_gemm_workspace_bytes", "vq_q8_gemm",
             "vq_q8_linear_workspace_bytes", "vq_q8_linear", "vq_expert_plan", "vq_q8_gemm_grouped", "vq_expert_combine",
-            "vq_q8_experts_workspace_bytes", "vq_q8_experts", "vq_block_norm")
+            "vq_q8_experts_workspace_bytes", "vq_q8_experts", "vq_block_norm", "vq_f8_quantize", "vq_f8_gemm_workspace_bytes",
+            "vq_f8_gemm", "vq_f8_linear_workspace_bytes", "vq_f8_linear", "vq_f8_mlp_workspace_bytes", "vq_f8_mlp",
+            "vq_rotate_heads")
 
 
 class Desc(ctypes.Structure):
@@ -127,6 +130,8 @@ def _load():
     lib.vq_assign.argtypes = [dp, vp, ctypes.c_int, vp, vp, vp, vp, vp, sz, vp]
     lib.vq_assign.restype = ctypes.c_int
     q8.bind(lib)
+    f8.bind(lib)
+    heads.bind(lib)
     return lib
 
 
@@ -541,3 +546,7 @@ from . import q8  # noqa: E402  (uses the helpers above)
 from .q8 import (NORM_LAYER, NORM_NONE, NORM_RMS, NormDesc, Q8Experts, Q8Linear, block_norm, expert_combine,  # noqa: E402,F401
                  expert_plan, q8_experts, q8_experts_workspace_bytes, q8_gemm, q8_gemm_grouped,
                  q8_gemm_workspace_bytes, q8_linear, q8_linear_workspace_bytes, q8_pad, q8_quantize, q8_row_bytes)
+from . import f8, heads  # noqa: E402
+from .f8 import (F8MLP, F8Linear, f8_blocks, f8_gemm, f8_gemm_workspace_bytes, f8_linear,  # noqa: E402,F401
+                 f8_linear_workspace_bytes, f8_mlp, f8_mlp_workspace_bytes, f8_pad, f8_quantize)
+from .heads import HeadsDesc, Rotary, rope_frequencies, rotate_heads  # noqa: E402,F401

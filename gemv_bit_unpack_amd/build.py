@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libvq.so")
 CEILINGS_SRC = os.path.join(PKG, "micro", "ceilings.hip")
 CEILINGS_BIN = os.path.join(PKG, "micro", "vq_ceilings")
 SOURCES = ["vq_host.cpp", "vq_dequant.hip", "vq_gemv.hip", "vq_gemv_sliced.hip", "vq_gemv_bucket.hip", "vq_gemm.hip", "vq_svq.hip", "vq_rht.hip",
-           "vq_assign.hip", "vq_svq_gemm.hip", "vq_gemm_gather.hip", "vq_q8_host.cpp", "vq_q8.hip", "vq_experts.hip", "vq_norm.hip"]
+           "vq_assign.hip", "vq_svq_gemm.hip", "vq_gemm_gather.hip", "vq_q8_host.cpp", "vq_q8.hip", "vq_experts.hip", "vq_norm.hip",
+           "vq_f8_host.cpp", "vq_f8.hip", "vq_heads_host.cpp", "vq_heads.hip"]
 ARCH = "gfx950"
 
 COMMON = [
@@ -39,9 +40,9 @@ def _hipcc() -> str:
     return cand if os.path.exists(cand) else "hipcc"
 
 
-# Per-unit additions.  vq_assign: matrix-core results go straight to VGPRs (the VALU reads
-# every one of them), instead of through the accumulation registers.
-EXTRA = {"vq_assign.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# Per-unit additions.  vq_assign and vq_f8: matrix-core results go straight to VGPRs (the VALU
+# reads every one of them), instead of through the accumulation registers.
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in ("vq_assign.hip", "vq_f8.hip")}
 
 
 def _compile(src: str) -> str:

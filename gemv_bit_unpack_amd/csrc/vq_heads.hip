@@ -1,0 +1,308 @@
+// vq_rotate_heads: norms of the queries' and keys' heads and their rotary positions, one pass over both.
+//
+//   v = N(x) over a head's values (identity, RMS or centred, weight and bias)
+//   pairs (a, b) of the rotated part:  a' = c (a cos t - b sin t),  b' = c (a sin t + b cos t),  t = position * frequency
+//
+// The angle is formed in fp64, in turns, and reduced there to an eighth of a turn: what is left goes to fp32 with an error
+// of 2^-27 turns at any position.  The sines of a workgroup's tokens are computed once, one pair per thread, and shared by
+// all heads in LDS.
+//
+// A head is held by L lanes (a power of two), 16 values each: 8 pairs of the rotated part, or 16 consecutive values of the
+// parts beside it.  Every value is read once and written once; the norm's sums go over the L lanes without LDS.
+#include "vq_device.h"
+#include "vq_f8_device.h"
+#include "vq_q8_device.h"
+
+namespace {
+
+using vqi::HeadsArgs;
+
+constexpr int kThreads = 256;
+constexpr int kItem = 16;       // values per lane and item
+constexpr int kSines = 1024;    // pairs of all tokens of a workgroup
+
+// Sum over groups of `lanes` consecutive lanes, the same bits in all of them.
+template <int CTRL>
+__device__ __forceinline__ float other(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+  if (lanes > 1) v += other<0xB1>(v);   // lane ^ 1
+  if (lanes > 2) v += other<0x4E>(v);   // lane ^ 2
+  if (lanes > 4) v += other<0x141>(v);  // the other four of 8
+  if (lanes > 8) v += other<0x140>(v);  // the other eight of 16
+  if (lanes > 16) v += __shfl_xor(v, 16, 64);
+  if (lanes > 32) v += __shfl_xor(v, 32, 64);
+  return v;
+}
+
+// Where a lane's item lies in a head: 8 values from `a` on and 8 from `b` on, `na` and `nb` of them there; `pair` is its
+// first pair, or -1 beside the rotated part.
+struct Item {
+  int32_t a, b, na, nb, pair;
+};
+__device__ __forceinline__ Item item_at(const HeadsArgs& h, int32_t i) {
+  Item r{0, 0, 0, 0, -1};
+  const int32_t half = h.rot / 2, front = (h.start + 15) / 16, turned = (half + 7) / 8;
+  int32_t at, end;
+  if (i < front) {
+    at = i * 16;
+    end = h.start;
+  } else if (i < front + turned) {
+    r.pair = (i - front) * 8;
+    const int32_t n = min(8, half - r.pair);
+    if (h.interleaved) {
+      at = h.start + 2 * r.pair;
+      end = at + 2 * n;
+    } else {
+      r.a = h.start + r.pair;
+      r.b = r.a + half;
+      r.na = r.nb = n;
+      return r;
+    }
+  } else {
+    at = h.start + h.rot + (i - front - turned) * 16;
+    end = h.dim;
+  }
+  r.a = at;
+  r.b = at + 8;
+  r.na = min(max(end - at, 0), 8);
+  r.nb = min(max(end - at - 8, 0), 8);
+  return r;
+}
+inline int32_t items_of(const HeadsArgs& h) {
+  return (h.start + 15) / 16 + (h.rot / 2 + 7) / 8 + (h.dim - h.start - h.rot + 15) / 16;
+}
+
+template <vq_dtype XT>
+struct Bits {
+  static constexpr int kWords = XT == VQ_F32 ? 8 : 4;
+  uint32_t v[2][kWords];
+};
+// `n` of 8 values at p; zeros behind.
+template <vq_dtype XT>
+__device__ __forceinline__ void load_bits(const char* p, int32_t n, uint32_t (&v)[Bits<XT>::kWords]) {
+  constexpr int es = XT == VQ_F32 ? 4 : 2;
+  if (n == 8) {
+    __builtin_memcpy(v, p, 8 * es);
+  } else {
+#pragma unroll
+    for (int k = 0; k < Bits<XT>::kWords; ++k) {
+      if constexpr (XT == VQ_F32) {
+        v[k] = k < n ? ((const uint32_t*)p)[k] : 0u;
+      } else {
+        v[k] = (2 * k < n ? ((const uint16_t*)p)[2 * k] : 0u) | (2 * k + 1 < n ? ((const uint16_t*)p)[2 * k + 1] : 0u) << 16;
+      }
+    }
+  }
+}
+template <vq_dtype XT>
+__device__ __forceinline__ float value(const uint32_t (&v)[Bits<XT>::kWords], int k) {
+  if constexpr (XT == VQ_F32) {
+    return __builtin_bit_cast(float, v[k]);
+  } else {
+    return vqd::x_to_f32<XT == VQ_F16 ? 0 : 1>(v[k / 2] >> (16 * (k & 1)));
+  }
+}
+__device__ __forceinline__ void load_vec(const void* p, vq_dtype t, int32_t at, int32_t n, float* f) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    f[k] = 0.f;
+    if (k < n)
+      f[k] = t == VQ_F32 ? ((const float*)p)[at + k]
+                         : t == VQ_F16 ? vqd::f16_to_f32(((const uint16_t*)p)[at + k]) : vqd::bf16_to_f32(((const uint16_t*)p)[at + k]);
+  }
+}
+__device__ __forceinline__ void store_part(char* row, vq_dtype t, int32_t at, int32_t n, const float* f) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = f[k];
+  if (t == VQ_F32) {
+    float* p = (float*)row + at;
+    if (n == 8) {
+      __builtin_memcpy(p, v, 32);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) p[k] = v[k];
+    }
+  } else {
+    uint16_t h[8];
+    vqd::narrow<8>(v, t, h);
+    uint16_t* p = (uint16_t*)row + at;
+    if (n == 8) {
+      __builtin_memcpy(p, h, 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) p[k] = h[k];
+    }
+  }
+}
+
+// A workgroup takes `tt` tokens (of batch * tokens, from blockIdx.x * tt on) and `per` heads (of queries and keys in a row,
+// from blockIdx.y * per on); its groups of `lanes` lanes take one head of one token after the other.  I items per lane.
+template <int I, int NORM, vq_dtype XT>
+__global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a, int32_t lanes, int32_t tt, int32_t per) {
+  __shared__ float cs[kSines], sn[kSines];
+  const int64_t all = (int64_t)a.batch * a.tokens;
+  const int64_t bt0 = (int64_t)blockIdx.x * tt;
+  const int32_t here = (int32_t)min((int64_t)tt, all - bt0);
+  const int32_t half = a.rot / 2;
+  const int32_t groups = kThreads / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  constexpr int es = XT == VQ_F32 ? 4 : 2;
+  const int ey = a.y_dtype == VQ_F32 ? 4 : 2;
+
+  for (int32_t i = threadIdx.x; i < here * half; i += kThreads) {
+    const int32_t tok = i / half, j = i - tok * half;
+    const int64_t bt = bt0 + tok;
+    const int64_t b = bt / a.tokens, at = b * a.pos_stride + (bt - b * a.tokens);
+    const double p = a.pos_64 ? (double)((const int64_t*)a.positions)[at] : (double)((const int32_t*)a.positions)[at];
+    const double turn = p * a.freqs[j];
+    const double r = turn - __builtin_rint(turn);
+    const double quarter = __builtin_rint(4.0 * r);
+    float s, c;
+    sincospif((float)(2.0 * (r - 0.25 * quarter)), &s, &c);  // up to a quarter of a half turn
+    const int q = (int)quarter & 3;
+    const float c1 = q & 1 ? s : c, s1 = q & 1 ? c : s;
+    cs[i] = (q == 1 || q == 2 ? -c1 : c1) * a.scale;
+    sn[i] = (q >= 2 ? -s1 : s1) * a.scale;
+  }
+  __syncthreads();
+
+  Item it[I];
+#pragma unroll
+  for (int n = 0; n < I; ++n) it[n] = item_at(a, lane + n * lanes);
+  const float inv_d = 1.0f / (float)a.dim;
+
+  for (int part = 0; part < 2; ++part) {
+    const int32_t first = part ? a.heads[0] : 0;  // of this part, among all heads
+    const int32_t h0 = max((int32_t)blockIdx.y * per - first, 0);
+    const int32_t h1 = min(((int32_t)blockIdx.y + 1) * per - first, a.heads[part]);
+    if (h0 >= h1) continue;
+    const int32_t count = h1 - h0, units = here * count;
+    float w[NORM ? I : 1][16], bias[NORM ? I : 1][16];
+    if constexpr (NORM) {
+#pragma unroll
+      for (int n = 0; n < I; ++n) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          w[n][k] = 1.f;
+          bias[n][k] = 0.f;
+        }
+        if (a.w[part]) {
+          load_vec(a.w[part], a.w_dtype, it[n].a, it[n].na, w[n]);
+          load_vec(a.w[part], a.w_dtype, it[n].b, it[n].nb, w[n] + 8);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[n][k] += a.w_offset;
+        }
+        if (a.b[part]) {
+          load_vec(a.b[part], a.w_dtype, it[n].a, it[n].na, bias[n]);
+          load_vec(a.b[part], a.w_dtype, it[n].b, it[n].nb, bias[n] + 8);
+        }
+      }
+    }
+    for (int32_t u0 = 0; u0 < units; u0 += groups) {
+      const int32_t u = u0 + group;
+      const bool there = u < units;  // idle lanes go along: the sums are over whole groups of lanes
+      const int32_t tok = there ? u / count : 0, h = there ? h0 + u - tok * count : h0;
+      const int64_t bt = bt0 + tok, b = bt / a.tokens, t = bt - b * a.tokens;
+      const char* x = (const char*)a.x[part] + (b * a.xs[part][0] + t * a.xs[part][1] + h * a.xs[part][2]) * es;
+      char* y = (char*)a.y[part] + (b * a.ys[part][0] + t * a.ys[part][1] + h * a.ys[part][2]) * ey;
+      float f[I][16];
+#pragma unroll
+      for (int n = 0; n < I; ++n) {
+        Bits<XT> raw;
+        load_bits<XT>(x + (int64_t)it[n].a * es, it[n].na, raw.v[0]);
+        load_bits<XT>(x + (int64_t)it[n].b * es, it[n].nb, raw.v[1]);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) f[n][k] = value<XT>(raw.v[k / 8], k % 8);
+      }
+      if constexpr (NORM != VQ_NORM_NONE) {
+        if constexpr (NORM == VQ_NORM_LAYER) {
+          float sum = 0.f;
+#pragma unroll
+          for (int n = 0; n < I; ++n)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum += f[n][k];  // zeros past the ends
+          const float mean = group_sum(sum, lanes) * inv_d;
+#pragma unroll
+          for (int n = 0; n < I; ++n)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[n][k] = k % 8 < (k < 8 ? it[n].na : it[n].nb) ? f[n][k] - mean : 0.f;
+        }
+        float sq = 0.f;
+#pragma unroll
+        for (int n = 0; n < I; ++n)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) sq = __builtin_fmaf(f[n][k], f[n][k], sq);
+        const float inv = 1.0f / __builtin_sqrtf(group_sum(sq, lanes) * inv_d + a.eps);
+#pragma unroll
+        for (int n = 0; n < I; ++n)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) f[n][k] = __builtin_fmaf(f[n][k] * inv, w[n][k], bias[n][k]);
+      }
+#pragma unroll
+      for (int n = 0; n < I; ++n) {
+        if (it[n].pair >= 0) {
+          const int32_t at = tok * half + it[n].pair;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int32_t j = at + (it[n].pair + k < half ? k : 0);
+            const float c = cs[j], s = sn[j];
+            float& p = a.interleaved ? f[n][2 * k] : f[n][k];
+            float& q = a.interleaved ? f[n][2 * k + 1] : f[n][8 + k];
+            const float p1 = __builtin_fmaf(p, c, -(q * s)), q1 = __builtin_fmaf(p, s, q * c);
+            p = p1;
+            q = q1;
+          }
+        }
+        if (there) {
+          store_part(y, a.y_dtype, it[n].a, it[n].na, f[n]);
+          store_part(y, a.y_dtype, it[n].b, it[n].nb, f[n] + 8);
+        }
+      }
+    }
+  }
+}
+
+template <int I, int NORM>
+void launch(const HeadsArgs& a, dim3 g, int32_t lanes, int32_t tt, int32_t per, hipStream_t st) {
+  switch (a.x_dtype) {
+    case VQ_F32: heads_kernel<I, NORM, VQ_F32><<<g, dim3(kThreads), 0, st>>>(a, lanes, tt, per); break;
+    case VQ_F16: heads_kernel<I, NORM, VQ_F16><<<g, dim3(kThreads), 0, st>>>(a, lanes, tt, per); break;
+    default: heads_kernel<I, NORM, VQ_BF16><<<g, dim3(kThreads), 0, st>>>(a, lanes, tt, per);
+  }
+}
+
+}  // namespace
+
+namespace vqi {
+
+vq_status launch_heads(const HeadsArgs& a, void* stream) {
+  hipStream_t st = (hipStream_t)stream;
+  const int32_t items = items_of(a);
+  int32_t lanes = 1;
+  while (lanes < items && lanes < 64) lanes *= 2;
+  if (items > 2 * lanes) return VQ_ERR_SHAPE;
+  const int64_t all = (int64_t)a.batch * a.tokens;
+  const int32_t heads = a.heads[0] + a.heads[1], groups = kThreads / lanes;
+  int32_t tt = 1, per = groups;
+  if (all >= 1024) {
+    per = heads;
+    tt = 4;
+  }
+  while (tt > 1 && tt * (a.rot / 2) > kSines) tt /= 2;
+  const int64_t gx = (all + tt - 1) / tt, gy = ((int64_t)heads + per - 1) / per;
+  if (gy > 65535 || !grid_ok(gx * gy, kThreads)) return VQ_ERR_SHAPE;
+  const dim3 g((uint32_t)gx, (uint32_t)gy);
+  const bool two = items > lanes;
+  switch (a.norm) {
+    case VQ_NORM_NONE: two ? launch<2, VQ_NORM_NONE>(a, g, lanes, tt, per, st) : launch<1, VQ_NORM_NONE>(a, g, lanes, tt, per, st); break;
+    case VQ_NORM_RMS: two ? launch<2, VQ_NORM_RMS>(a, g, lanes, tt, per, st) : launch<1, VQ_NORM_RMS>(a, g, lanes, tt, per, st); break;
+    default: two ? launch<2, VQ_NORM_LAYER>(a, g, lanes, tt, per, st) : launch<1, VQ_NORM_LAYER>(a, g, lanes, tt, per, st);
+  }
+  return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP;
+}
+
+}  // namespace vqi

@@ -239,4 +239,67 @@ vq_status launch_expert_combine(int32_t tokens, int32_t top, int32_t n, int32_t 
                                 const int32_t* pos, const float* p, void* y, vq_dtype y_dtype, void* stream,
                                 bool check_only = false);
 
+// ---- 8-bit floats (vq_f8_*) and the heads' pass (vq_rotate_heads) ----
+// Columns and weight rows of a block with one scale.
+constexpr int32_t kF8Block = 128;
+constexpr int32_t kF8MaxK = 65536;
+constexpr int64_t f8_blocks(int64_t n) { return (n + kF8Block - 1) / kF8Block; }
+
+// Rows or 128-row blocks of x [rows][k] to e4m3 with block scales (validated arguments; vq_f8.hip).
+struct F8QuantArgs {
+  int32_t rows, k;
+  const void* x;
+  vq_dtype x_dtype;
+  int64_t ldx;  // elements
+  uint8_t* q;   // [rows][q8_row_bytes(k)]
+  float* s;     // tokens: [f8_blocks(k)][rows]; weights: [f8_blocks(rows)][f8_blocks(k)]
+};
+vq_status launch_f8_tokens(const F8QuantArgs& a, void* stream, bool check_only = false);
+vq_status launch_f8_weights(const F8QuantArgs& a, void* stream);
+
+// A product with block scales (validated arguments; vq_f8.hip).
+struct F8Args {
+  int32_t m, n, k;   // n outputs (with the gate: w has 2 n rows)
+  const uint8_t* q;  // [m][q8_row_bytes(k)] e4m3, or nullptr: the tokens are cut to 8 bits inside the kernel
+  const float* s;    // [f8_blocks(k)][m]
+  const void* x;     // q == nullptr: [m][k]
+  vq_dtype x_dtype;
+  int64_t ldx;
+  const uint8_t* w;      // [n or 2 n][q8_row_bytes(k)] e4m3
+  const float* sw;       // [f8_blocks(n), twice with the gate][f8_blocks(k)]
+  const uint16_t* bias;  // fp16 [n or 2 n] or nullptr
+  int32_t gated;         // y = silu(g) u, g and u the two halves of w's rows
+  int32_t wide;          // the products' operands go to fp16, for sums that are exact to fp32 (fp32 outputs)
+  void* y;               // [m][n], or nullptr: yq and ys take the outputs in 8 bits
+  vq_dtype y_dtype;
+  uint8_t* yq;  // [m][q8_row_bytes(n)]
+  float* ys;    // [f8_blocks(n)][m]
+  float* part;  // [splits][m][n] fp32 partial sums (splits > 1)
+  int32_t splits;
+};
+// K splits that a product of this shape uses; its workspace is splits * m * n fp32 where splits > 1.
+int32_t f8_splits(int32_t m, int32_t n, int32_t k, bool gated);
+// Whether a product of this shape cuts its tokens to 8 bits inside the kernel.
+bool f8_cuts_inside(int32_t m, int32_t n, int32_t k, bool gated);
+// Whether a gated product of this shape can write its outputs in 8 bits (yq, ys).
+bool f8_writes_q(int32_t m, int32_t n, int32_t k);
+vq_status launch_f8(const F8Args& a, void* stream, bool check_only = false);
+
+// Norms and rotation of heads (validated arguments; vq_heads.hip).
+struct HeadsArgs {
+  int32_t batch, tokens, heads[2], dim, rot, start, interleaved, norm;
+  const void* x[2];  // queries and keys: [batch][tokens][heads][dim]
+  void* y[2];
+  int64_t xs[2][3], ys[2][3];  // strides of batch, tokens and heads in elements
+  vq_dtype x_dtype, y_dtype, w_dtype;
+  const void* positions;
+  int32_t pos_64;      // int64 positions, else int32
+  int64_t pos_stride;  // of batch, in elements; 0: the same for all
+  const double* freqs;  // [rot / 2] turns per position
+  float scale;          // on the rotated values
+  const void *w[2], *b[2];  // [dim] or nullptr
+  float eps, w_offset;
+};
+vq_status launch_heads(const HeadsArgs& a, void* stream);
+
 }  // namespace vqi

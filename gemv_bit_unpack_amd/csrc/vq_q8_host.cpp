@@ -2,6 +2,7 @@
 // entry points vq_q8_*, vq_expert_* and vq_block_norm.
 #include <cstring>
 
+#include "vq_host_checks.h"
 #include "vq_internal.h"
 
 namespace vqi {
@@ -10,22 +11,7 @@ namespace {
 constexpr int64_t kMaxPairs = (int64_t)1 << 30;
 constexpr int32_t kMaxExperts = 4096;
 
-bool valid_dtype(vq_dtype t) { return t == VQ_F16 || t == VQ_BF16 || t == VQ_F32; }
-size_t size_of(vq_dtype t) { return t == VQ_F32 ? 4 : 2; }
 bool valid_k(int32_t k) { return k >= 1 && k <= kQ8MaxK; }
-size_t padded(size_t n) { return (n + 255) / 256 * 256; }
-bool misaligned(const void* p, size_t a) { return p && !aligned(p, a); }
-
-// Consecutive 256-byte aligned pieces of a workspace.
-struct Pieces {
-  uint8_t* base;
-  size_t at = 0;
-  void* take(size_t n) {
-    void* p = base ? base + at : nullptr;
-    at += padded(n);
-    return p;
-  }
-};
 
 size_t part_bytes(int32_t m, int32_t n, int32_t k, int32_t* splits) {
   *splits = m > 0 && n > 0 ? q8_splits(m, n, k) : 1;

@@ -493,6 +493,83 @@ vq_status vq_block_norm(const vq_norm_desc* desc, const void* z, const void* h, 
                         const void* pre_w, const void* pre_b, const void* gate, void* r, void* x, void* q, float* s,
                         void* stream);
 
+/*
+ * Layers in 8-bit floating point, as checkpoints with block scales keep them.  The values are e4m3 (4 bits of exponent, 3
+ * of fraction, largest 448, no infinities), in rows of vq_q8_row_bytes(k) bytes with zero pads as above; one fp32 scale
+ * stands for each block: of a token, 128 consecutive columns; of weights, 128 rows by 128 columns.  Blocks at the ends are
+ * short.  value = q * s.  1 <= k <= 65536.  Blocks are written with
+ *     s = fp32(max|x| / 448),  q = fp32(x / s) rounded to the nearest e4m3 value, ties to even, within +-448.
+ * A zero block has s = 0 and q = 0; one that holds an infinity or a NaN has s = NaN and q = 0.  A block's products are
+ * summed by the matrix instruction, the blocks in fp32, in an order that the shape fixes: equal calls give equal bits.
+ */
+
+/* x [rows][k] (row stride ldx >= k elements; fp16, bf16 or fp32, element-aligned) -> q [rows][vq_q8_row_bytes(k)] (16-byte
+ * aligned) and s fp32.  block_rows 1, tokens: s [ceil(k / 128)][rows], so that a block's scales of neighbouring tokens are
+ * neighbours.  block_rows 128, weights: s [ceil(rows / 128)][ceil(k / 128)].  Others: VQ_ERR_UNSUPPORTED. */
+vq_status vq_f8_quantize(int32_t rows, int32_t k, int32_t block_rows, const void* x, vq_dtype x_dtype, int64_t ldx, void* q,
+                         float* s, void* stream);
+
+/* y [M][N] = x w^T (+ bias) of tokens q, s and weights w, sw of K columns as above (16-byte aligned), bias fp16 or NULL,
+ * y_dtype fp16, bf16 or fp32, any M >= 0.
+ *   gated == 0: w [N] rows, sw [ceil(N / 128)][ceil(K / 128)], bias [N]
+ *   gated == 1: y = silu(g) * u, g the product with rows 0 .. N - 1 of w and u with rows N .. 2 N - 1; each half has
+ *               blocks of its own: sw [2 ceil(N / 128)][ceil(K / 128)], the gate's first; bias [2 N]
+ * `workspace` (256-byte aligned) holds the fp32 partial sums of products that cut K over the CUs; NULL computes y without
+ * cutting it (0 bytes: there is nothing to cut). */
+vq_status vq_f8_gemm_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated, size_t* nbytes);
+vq_status vq_f8_gemm(int32_t M, int32_t N, int32_t K, const void* q, const float* s, const void* w, const float* sw,
+                     const void* bias, int32_t gated, void* y, vq_dtype y_dtype, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* vq_f8_gemm on x [M][K] (row stride ldx elements, fp16, bf16 or fp32) cut to 8 bits inside the call.  The workspace is
+ * required where vq_f8_linear_workspace_bytes is not 0 (few tokens are cut inside the product and take none). */
+vq_status vq_f8_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t gated, size_t* nbytes);
+vq_status vq_f8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype x_dtype, int64_t ldx, const void* w,
+                       const float* sw, const void* bias, int32_t gated, void* y, vq_dtype y_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* A gated feed-forward layer: for x [M][D] (row stride ldx)
+ *   y = W_out h,  h = silu(g) * u cut to 8 bits from its fp32 values, in blocks of 128 columns,  (g, u) = W_in x
+ * w_in [2 I] rows of D columns (gate rows first) and s_in as for the gated product, w_out [D] rows of I columns, s_out
+ * [ceil(D / 128)][ceil(I / 128)]; y [M][D].  The workspace is required. */
+vq_status vq_f8_mlp_workspace_bytes(int32_t M, int32_t D, int32_t I, size_t* nbytes);
+vq_status vq_f8_mlp(int32_t M, int32_t D, int32_t I, const void* x, vq_dtype x_dtype, int64_t ldx, const void* w_in,
+                    const float* s_in, const void* w_out, const float* s_out, void* y, vq_dtype y_dtype, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+#define VQ_HEADS_MAX 65536
+#define VQ_HEADS_MAX_DIM 1024
+
+/* Shapes, types and constants of vq_rotate_heads.  Strides are in elements, of batch, token and head; a head's values are
+ * consecutive.  None is negative; an output's heads do not overlap. */
+typedef struct vq_heads_desc {
+  int32_t batch, tokens;
+  int32_t q_heads, k_heads;  /* 0: no such tensor; at most VQ_HEADS_MAX */
+  int32_t dim;               /* 1 <= dim <= VQ_HEADS_MAX_DIM */
+  int32_t rot, start;        /* the rotated part of a head: values start .. start + rot - 1, rot even (0: none) */
+  int32_t interleaved;       /* pair j is values (2 j, 2 j + 1) of the part, else (j, j + rot / 2) */
+  int32_t norm;              /* vq_norm_kind */
+  vq_dtype x_dtype, y_dtype; /* inputs and outputs: fp16, bf16 or fp32 */
+  vq_dtype w_dtype;          /* norm weights and biases */
+  int32_t positions_64;      /* positions are int64, else int32 */
+  int64_t position_stride;   /* of batch; 0: all batches at the same positions */
+  int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3];
+  float scale;               /* on the rotated values */
+  float eps, w_offset;       /* the norm multiplies by w_offset + w */
+} vq_heads_desc;
+
+/* Norms of the heads of queries and keys, and their rotary positions, in one pass: for each head, in fp32 and rounded once
+ * at the store,
+ *   v = N(x)                                       over the head's dim values, N as in vq_block_norm
+ *   a' = scale (a cos t - b sin t),  b' = scale (a sin t + b cos t)   for the pairs (a, b) of the rotated part
+ * and v elsewhere, with t = 2 pi positions[batch][token] freqs[j].  freqs: device, double [rot / 2], turns per position;
+ * positions: device, any sign (-p undoes p), exact up to 2^53: the angle is formed and reduced in fp64.  Weights and biases
+ * [dim] may each be NULL (1, 0), and are not taken without a norm.  An output may be its input itself where type and
+ * strides are the same; otherwise no output overlaps an input.  Pointers are element-aligned. */
+vq_status vq_rotate_heads(const vq_heads_desc* desc, const void* q, const void* k, const void* positions,
+                          const double* freqs, const void* q_w, const void* q_b, const void* k_w, const void* k_b,
+                          void* q_out, void* k_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
