@@ -100,19 +100,19 @@ __global__ __launch_bounds__(256) void f8_tokens_kernel(F8QuantArgs a) {
   const int64_t ld = vqi::q8_row_bytes(a.k);
   const int32_t blocks = (int32_t)(ld / kStep);
   const int32_t b0 = (int32_t)blockIdx.y * kQuantCols;
-  float f[kQuantCols][8];
+  vqd::Run<XT, 8> raw[kQuantCols];
 #pragma unroll
-  for (int c = 0; c < kQuantCols; ++c) vqd::load_f32<XT, 8>(x, (b0 + c) * kStep + lane16 * 8, a.k, f[c]);
+  for (int c = 0; c < kQuantCols; ++c) raw[c] = vqd::load_run<XT, 8>(x, (b0 + c) * kStep + lane16 * 8, a.k);
 #pragma unroll
   for (int c = 0; c < kQuantCols; ++c) {
     if (b0 + c >= blocks) break;
+    float f[8];
+    vqd::widen(raw[c], f);
     uint32_t big = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) big = max(big, vqd::abs_bits(f[c][k]));
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) big = max(big, (uint32_t)__shfl_xor((int)big, o, 64));
-    const vqd::Q8Scale sc = vqd::f8_scale(big);
-    const uint2 v = make_uint2(vqd::f8_pack4(f[c], sc), vqd::f8_pack4(f[c] + 4, sc));
+    for (int k = 0; k < 8; ++k) big = max(big, vqd::abs_bits(f[k]));
+    const vqd::Q8Scale sc = vqd::f8_scale(vqd::group_max<16>(big));
+    const uint2 v = make_uint2(vqd::f8_pack4(f, sc), vqd::f8_pack4(f + 4, sc));
     *(uint2*)(a.q + (int64_t)row * ld + (b0 + c) * kStep + lane16 * 8) = v;
     if (lane16 == 0) a.s[(int64_t)(b0 + c) * a.rows + row] = sc.s;
   }
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256) void f8_weights_kernel(F8QuantArgs a) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int32_t r = row0 + 16 * j;
-    vqd::load_f32<XT, 8>((const char*)a.x + (int64_t)min(r, end - 1) * a.ldx * es, kb * kStep + col, a.k, f[j]);
+    vqd::widen(vqd::load_run<XT, 8>((const char*)a.x + (int64_t)min(r, end - 1) * a.ldx * es, kb * kStep + col, a.k), f[j]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) big = max(big, vqd::abs_bits(f[j][k]));  // a row past the end repeats the last one
   }
@@ -159,16 +159,17 @@ __device__ __forceinline__ void to_lds4(const float* g, uint8_t* l) {
                                    (__attribute__((address_space(3))) void*)l, 4, 0, 0);
 }
 
-// LDS of a tile: NB steps of its rows and its tokens' scales, the scales of the weights' blocks (two rows of at most 512),
-// and the tokens' largest values of the 8-bit epilogue.
-template <int BM, int BN, int NB>
-constexpr int kTileLds = NB * ((BM + BN) * kStep + BM * 4);
+// Bytes of a step in LDS: its rows and its tokens' scales (64 at least, what a wavefront's load brings).
+constexpr int step_bytes(int bm, int bn) { return (bm + bn) * kStep + (bm < 64 ? 64 : bm) * 4; }
 
-// One tile: WM x WN wavefronts compute BM rows (row0 ..) by BN weight rows (with the gate: BN / 2 outputs).  Each
-// wavefront's weight rows are 16 NI consecutive ones (8 NI outputs of gate and up rows with the gate), dealt to its NI
-// blocks so that a lane ends with 4 NI (2 NI) consecutive outputs of one token.
+// One tile: KG groups of WM x WN wavefronts, each with its share of K and its own NB steps in LDS, compute BM rows (row0
+// ..) by BN weight rows (with the gate: BN / 2 outputs).  Each wavefront's weight rows are 16 NI consecutive ones (8 NI
+// outputs of gate and up rows with the gate), dealt to its NI blocks so that a lane ends with 4 NI (2 NI) consecutive
+// outputs of one token.
 // OUTQ: the outputs in 8 bits (with the gate, BN / 2 = 128 outputs: one block).
-template <int BM, int BN, int WM, int WN, int NB, bool WIDE, bool GATED, bool SPLIT, bool OUTQ>
+// lds: KG * NB steps.  sbs: the scales of the weights' blocks, two rows of at most 512.  tops: the tokens' largest values
+// of the 8-bit epilogue.
+template <int BM, int BN, int WM, int WN, int NB, int KG, bool WIDE, bool GATED, bool SPLIT, bool OUTQ>
 __device__ __forceinline__ void tile(const F8Args& a, int32_t row0, int32_t n0, uint8_t* lds, float* sbs, float* tops) {
   constexpr int kWaves = WM * WN;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
@@ -176,29 +177,39 @@ __device__ __forceinline__ void tile(const F8Args& a, int32_t row0, int32_t n0, 
   constexpr int TL = BM / 8 / kWaves, WL = BN / 8 / kWaves;  // 8-row loads per wavefront and step
   constexpr int SG = (BM + 63) / 64;                         // groups of 64 token scales
   constexpr int kRows = (BM + BN) * kStep;
-  constexpr int kBuf = kRows + BM * 4;
+  constexpr int kBuf = step_bytes(BM, BN);
+  // steps in LDS: one is read while NB - 1 are on their way; vmcnt of a wavefront whose loads of one step more than the
+  // next may be outstanding
   constexpr int kLater = (NB - 2) * (TL + WL + 1);
   static_assert(NB >= 2 && kLater < 64, "the wait counter holds 6 bits");
   constexpr int kWaitNext = 0x0070 | (kLater & 15) | (kLater >> 4) << 14;  // and lgkmcnt(0)
   static_assert(TL * 8 * kWaves == BM && WL * 8 * kWaves == BN, "whole loads");
-  static_assert(BM % 64 == 0 && SG <= kWaves, "each wavefront loads one group of scales");
+  static_assert(SG <= kWaves, "each wavefront loads one group of scales");
   static_assert(!GATED || NI % 2 == 0, "gate and up blocks in one wavefront");
   static_assert(!OUTQ || (GATED && BN == 256 && WN * NO * 16 == 128), "a block of outputs per tile");
+  // small tiles read the next step's fragments while they multiply this one's
+  constexpr bool AHEAD = MI + NI <= 6;
+  static_assert(KG == 1 || (KG == 2 && AHEAD && !SPLIT && !OUTQ && MI * NI * 1024 * kWaves <= NB * kBuf), "sums of two groups");
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = all_wave % kWaves, group = all_wave / kWaves;
+  lds += group * NB * kBuf;
   const int wm = wave / WN, wn = wave % WN;
   const int col = lane & 15, grp = lane >> 4;
   const int64_t ld = vqi::q8_row_bytes(a.k);
   const int32_t blocks = (int32_t)(ld / kStep);
   const int32_t end = min(a.m, row0 + BM);
 
-  int32_t kt0 = 0, kt1 = blocks;
+  int32_t first = 0, last = blocks;
   if constexpr (SPLIT) {
-    kt0 = (int32_t)((int64_t)blocks * blockIdx.y / a.splits);
-    kt1 = (int32_t)((int64_t)blocks * (blockIdx.y + 1) / a.splits);
+    first = (int32_t)((int64_t)blocks * blockIdx.y / a.plan.splits);
+    last = (int32_t)((int64_t)blocks * (blockIdx.y + 1) / a.plan.splits);
   }
-  const int32_t n = kt1 - kt0;
+  // steps of each group of wavefronts; the second may have one less
+  const int32_t n = (last - first + KG - 1) / KG;
+  const int32_t kt0 = first + group * n;
+  const int32_t mine = KG == 1 ? n : min(n, last - kt0);
 
   // this lane's 16-byte piece of every load: row p of the tile, chunk lane % 8 of its LDS row, which holds chunk
   // (lane % 8) ^ (p / 2 % 8) of the matrix row (reads of 16 rows at one chunk then fall on all 64 banks)
@@ -232,19 +243,31 @@ __device__ __forceinline__ void tile(const F8Args& a, int32_t row0, int32_t n0, 
     to_lds4(gs, lds + buf * kBuf + kRows + wave % SG * 256);  // some twice, the same values
     gs += a.m;
   };
-#pragma unroll
-  for (int b = 0; b < NB - 1; ++b)
-    if (b < n) fetch(b);
-
-  // the weights' scales of the steps: with the gate a row for each half, else one for each 128 weight rows
+  // the weights' scales of the steps: with the gate a row for each half, else one for each 128 weight rows.  Asked for
+  // before the first steps and put down behind them: no load waits for another
   const int32_t nblocks = (int32_t)vqi::f8_blocks(a.n);
   constexpr int kScaleRows = GATED || BN > 128 ? 2 : 1;
-  for (int32_t i = threadIdx.x; i < n * kScaleRows; i += 64 * kWaves) {
-    const int32_t r = i / n, k = i - r * n;
+  constexpr int kThreads = 64 * kWaves * KG;
+  constexpr int kPer = (512 + kThreads - 1) / kThreads;
+  const int32_t all = last - first;
+  float sv[kScaleRows][kPer];
+#pragma unroll
+  for (int r = 0; r < kScaleRows; ++r) {
     const int32_t nb = GATED ? n0 / 128 + r * nblocks : min(n0 / 128 + r, nblocks - 1);
-    sbs[r * 512 + k] = a.sw[(int64_t)nb * blocks + kt0 + k];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      sv[r][i] = a.sw[(int64_t)nb * blocks + first + min((int32_t)threadIdx.x + i * kThreads, all - 1)];
   }
-  const float* const sb0 = sbs + (GATED ? 0 : (n0 % 128 + wn * 16 * NI) / 128 * 512);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int b = 0; b < NB - 1; ++b)
+    if (b < mine) fetch(b);
+#pragma unroll
+  for (int r = 0; r < kScaleRows; ++r)
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if ((int32_t)threadIdx.x + i * kThreads < all) sbs[r * 512 + threadIdx.x + i * kThreads] = sv[r][i];
+  const float* const sb0 = sbs + (GATED ? 0 : (n0 % 128 + wn * 16 * NI) / 128 * 512) + (kt0 - first);
 
   v4f acc[MI][NI];
 #pragma unroll
@@ -256,62 +279,153 @@ __device__ __forceinline__ void tile(const F8Args& a, int32_t row0, int32_t n0, 
   const int lw = BM * kStep + (wn * NI * 16 + col) * kStep;
   const int c0 = (grp ^ ((col >> 1) & 7)) * 16;
   auto frag = [&](int at) { return join<WIDE>(*(const v4i*)(lds + at + c0), *(const v4i*)(lds + at + (c0 ^ 64))); };
+  auto token_scale = [&](int at, int i) { return *(const float*)(lds + at + kRows + (wm * MI * 16 + i * 16 + col) * 4); };
+  auto add = [&](int i, const v4f (&p)[NI], float s, float sg, float su) {
+    const float s0 = s * sg, s1 = s * su;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[j][r], GATED && j >= NO ? s1 : s0, acc[i][j][r]);
+      asm volatile("" : "+v"(acc[i][j]));  // here, and not after the step's last product
+    }
+  };
+  // its part of step kt is in LDS (steps after that may still be on their way), its last reads are done
+  auto arrived = [&](int32_t kt) {
+    if (kt + NB - 2 < mine) {
+      __builtin_amdgcn_s_waitcnt(kWaitNext);
+    } else {
+      __builtin_amdgcn_s_waitcnt(0x0070);
+    }
+  };
 
-  if (NB - 1 <= n) {
-    __builtin_amdgcn_s_waitcnt(kWaitNext);  // this wavefront's part of the first step is in LDS
-  } else {
-    __builtin_amdgcn_s_waitcnt(0x0070);
-  }
-  __syncthreads();  // and everyone's, and the scales
-  if (NB - 1 < n) fetch(NB - 1);
+  arrived(0);
+  meet();  // and everyone's, and the scales
+  if (NB - 1 < mine) fetch(NB - 1);
   int buf = 0;
-  for (int32_t kt = 0; kt < n; ++kt) {
-    const int at = buf * kBuf;
-    Frag<WIDE> w[NI], t[2];
-#pragma unroll
-    for (int j = 0; j < NI; ++j) w[j] = frag(at + lw + j * 16 * kStep);
-    t[0] = frag(at + lt);
-    const float sg = sb0[kt], su = GATED ? sbs[512 + kt] : 0.f;
-    float s[MI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i) s[i] = *(const float*)(lds + at + kRows + (wm * MI * 16 + i * 16 + col) * 4);
-    v4f p[2][NI];
-    auto add = [&](int i) {
-      const float s0 = s[i] * sg, s1 = s[i] * su;
+  // the next step may be read, this one overwritten
+  auto next = [&](int32_t kt) {
+    arrived(kt + 1);
+    meet();
+    if (kt + NB < mine) fetch(buf);
+    buf = buf + 1 == NB ? 0 : buf + 1;
+  };
+  if constexpr (AHEAD) {
+    v4i rw[2][NI][2], rt[2][MI][2];
+    float s[2][MI], sg[2], su[2];
+    auto read = [&](int set, int32_t kt) {
+      const int at = buf * kBuf;
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
+        rw[set][j][0] = *(const v4i*)(lds + at + lw + j * 16 * kStep + c0);
+        rw[set][j][1] = *(const v4i*)(lds + at + lw + j * 16 * kStep + (c0 ^ 64));
+      }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[i & 1][j][r], GATED && j >= NO ? s1 : s0, acc[i][j][r]);
-        asm volatile("" : "+v"(acc[i][j]));  // here, and not after the step's last product
+      for (int i = 0; i < MI; ++i) {
+        rt[set][i][0] = *(const v4i*)(lds + at + lt + i * 16 * kStep + c0);
+        rt[set][i][1] = *(const v4i*)(lds + at + lt + i * 16 * kStep + (c0 ^ 64));
+        s[set][i] = token_scale(at, i);
+      }
+      sg[set] = sb0[kt];
+      su[set] = GATED ? sb0[512 + kt] : 0.f;
+    };
+    auto step = [&](int set, int32_t kt) {
+      if (kt + 1 < n) {
+        next(kt);
+        read(1 - set, min(kt + 1, mine - 1));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (KG == 1 || kt < mine) {
+        Frag<WIDE> w[NI];
+#pragma unroll
+        for (int j = 0; j < NI; ++j) w[j] = join<WIDE>(rw[set][j][0], rw[set][j][1]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const Frag<WIDE> t = join<WIDE>(rt[set][i][0], rt[set][i][1]);
+          v4f p[NI];
+#pragma unroll
+          for (int j = 0; j < NI; ++j) p[j] = multiply<WIDE>(w[j], t);
+          add(i, p, s[set][i], sg[set], su[set]);
+        }
       }
     };
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if (i + 1 < MI) t[(i + 1) & 1] = frag(at + lt + (i + 1) * 16 * kStep);
-#pragma unroll
-      for (int j = 0; j < NI; ++j) p[i & 1][j] = multiply<WIDE>(w[j], t[i & 1]);
-      if (i > 0) add(i - 1);
-      // the row's fragment on its way first, then each product with its share of the additions of the row before
-      if (i + 1 < MI) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-#pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        __builtin_amdgcn_sched_group_barrier(0x008, WIDE ? 4 : 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 4 + (WIDE ? 4 : 0), 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+    read(0, 0);
+    int32_t kt = 0;
+    for (; kt + 2 <= n; kt += 2) {
+      step(0, kt);
+      step(1, kt + 1);
     }
-    add(MI - 1);
-    if (kt + 1 < n) {
-      // its part of the next step is in LDS (steps after that may still be on their way), its last reads are done
-      if (kt + NB - 1 < n) {
-        __builtin_amdgcn_s_waitcnt(kWaitNext);
-      } else {
-        __builtin_amdgcn_s_waitcnt(0x0070);
+    if (kt < n) step(0, kt);
+  } else {
+    // a step's weights and first token block are asked for behind the last products of the step before
+    static_assert(MI % 2 == 0, "the first token block's place is free by then");
+    v4i rw[NI][2], rt[2];
+    float s[MI], sg, su;
+    auto head = [&](int32_t kt) {
+      const int at = buf * kBuf;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) rt[h] = *(const v4i*)(lds + at + lt + (c0 ^ (64 * h)));
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rw[j][h] = *(const v4i*)(lds + at + lw + j * 16 * kStep + (c0 ^ (64 * h)));
+#pragma unroll
+      for (int i = 0; i < MI; ++i) s[i] = token_scale(at, i);
+      sg = sb0[kt];
+      su = GATED ? sb0[512 + kt] : 0.f;
+    };
+    auto step = [&](int32_t kt, bool more) {
+      const int at = buf * kBuf;
+      Frag<WIDE> w[NI], t[2];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) w[j] = join<WIDE>(rw[j][0], rw[j][1]);
+      t[0] = join<WIDE>(rt[0], rt[1]);
+      v4f p[2][NI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if (i + 1 < MI) {
+          t[(i + 1) & 1] = frag(at + lt + (i + 1) * 16 * kStep);
+        } else if (more) {
+          next(kt);
+        }
+#pragma unroll
+        for (int j = 0; j < NI; ++j) p[i & 1][j] = multiply<WIDE>(w[j], t[i & 1]);
+        if (i > 0) add(i - 1, p[(i - 1) & 1], s[i - 1], sg, su);
+        // the row's fragment on its way first, then each product with its share of the additions of the row before
+        if (i + 1 < MI) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x008, WIDE ? 4 : 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4 + (WIDE ? 4 : 0), 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      meet();  // and everyone's: the next step may be read, this one overwritten
-      if (kt + NB < n) fetch(buf);
-      buf = buf + 1 == NB ? 0 : buf + 1;
+      const float sl = s[MI - 1], gl = sg, ul = su;
+      if (more) {
+        head(kt + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      add(MI - 1, p[(MI - 1) & 1], sl, gl, ul);
+    };
+    head(0);
+    for (int32_t kt = 0; kt + 1 < n; ++kt) step(kt, true);
+    if (n > 0) step(n - 1, false);
+  }
+  if constexpr (KG == 2) {  // the second group's sums join the first's
+    v4f* const sums = (v4f*)(lds + (1 - group) * NB * kBuf) + wave * MI * NI * 64 + lane;
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    meet();  // no one reads a step any more
+    if (group == 1) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) sums[(i * NI + j) * 64] = acc[i][j];
     }
+    __syncthreads();
+    if (group == 1) return;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] += sums[(i * NI + j) * 64];
   }
 
   // outputs: lane = token row0 + .., 4 NO consecutive channels
@@ -388,13 +502,14 @@ __device__ __forceinline__ void tile(const F8Args& a, int32_t row0, int32_t n0, 
   }
 }
 
-template <int BM, int BN, int WM, int WN, int NB, bool WIDE, bool GATED, bool SPLIT>
-__global__ __launch_bounds__(64 * WM * WN) void f8_tile_kernel(F8Args a, int32_t nt, int32_t mt_count) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kTileLds<BM, BN, NB>];
-  __shared__ float sbs[(GATED || BN > 128 ? 2 : 1) * 512];
+template <int BM, int BN, int WM, int WN, int NB, int KG, bool WIDE, bool GATED, bool SPLIT>
+__global__ __launch_bounds__(64 * WM * WN * KG) void f8_tile_kernel(F8Args a, int32_t nt, int32_t mt_count) {
+  // one array: with more than one the compiler waits for all loads to LDS before each read of it
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NB * step_bytes(BM, BN) + (GATED || BN > 128 ? 4096 : 2048)];
+  float* const sbs = (float*)(lds + KG * NB * step_bytes(BM, BN));
   int32_t mt, nti;
   if (!place((int32_t)blockIdx.x, mt_count * nt, mt_count, nt, mt, nti)) return;
-  tile<BM, BN, WM, WN, NB, WIDE, GATED, SPLIT, false>(a, mt * BM, nti * (GATED ? BN / 2 : BN), lds, sbs, nullptr);
+  tile<BM, BN, WM, WN, NB, KG, WIDE, GATED, SPLIT, false>(a, mt * BM, nti * (GATED ? BN / 2 : BN), lds, sbs, nullptr);
 }
 
 // 8 wavefronts, one workgroup per CU: 256 x 256 tiles, or 128 x 256 ones where the operands go to fp16 (their fragments
@@ -402,15 +517,16 @@ __global__ __launch_bounds__(64 * WM * WN) void f8_tile_kernel(F8Args a, int32_t
 // over the 256 CUs if at most half of them have a tile in it: two half tiles for each then take half a round.
 template <bool WIDE, bool GATED, bool OUTQ>
 __global__ __launch_bounds__(512) void f8_big_kernel(F8Args a, int32_t nt, int32_t mt_count) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[WIDE ? kTileLds<128, 256, 3> : kTileLds<256, 256, 2>];
-  __shared__ float sbs[2 * 512];
-  __shared__ float tops[OUTQ ? 4 * (WIDE ? 128 : 256) : 1];
+  constexpr int kSteps = WIDE ? 3 * step_bytes(128, 256) : 2 * step_bytes(256, 256);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSteps + 4096 + (OUTQ ? 16 * (WIDE ? 128 : 256) : 0)];
+  float* const sbs = (float*)(lds + kSteps);
+  float* const tops = sbs + 1024;
   const int32_t total = mt_count * nt;
   const int32_t id = (int32_t)blockIdx.x;
   int32_t mt, nti, part = 0;
   if constexpr (WIDE) {
     if (!place(id, total, mt_count, nt, mt, nti)) return;
-    tile<128, 256, 2, 4, 3, true, GATED, false, OUTQ>(a, mt * 128, nti * (GATED ? 128 : 256), lds, sbs, tops);
+    tile<128, 256, 2, 4, 3, 1, true, GATED, false, OUTQ>(a, mt * 128, nti * (GATED ? 128 : 256), lds, sbs, tops);
   } else {
     const int32_t rest = total % 256;
     const int32_t full = rest <= 128 ? total - rest : total;  // ids from the next multiple of 8 on are halves
@@ -427,9 +543,9 @@ __global__ __launch_bounds__(512) void f8_big_kernel(F8Args a, int32_t nt, int32
     const int32_t row0 = mt * 256 + part * 128, n0 = nti * (GATED ? 128 : 256);
     if (row0 >= a.m) return;
     if (half || a.m - row0 <= 128) {
-      tile<128, 256, 2, 4, 2, false, GATED, false, OUTQ>(a, row0, n0, lds, sbs, tops);
+      tile<128, 256, 2, 4, 2, 1, false, GATED, false, OUTQ>(a, row0, n0, lds, sbs, tops);
     } else {
-      tile<256, 256, 2, 4, 2, false, GATED, false, OUTQ>(a, row0, n0, lds, sbs, tops);
+      tile<256, 256, 2, 4, 2, 1, false, GATED, false, OUTQ>(a, row0, n0, lds, sbs, tops);
     }
   }
 }
@@ -446,14 +562,14 @@ __global__ __launch_bounds__(256) void f8_join_kernel(F8Args a) {
   float v[4] = {0.f, 0.f, 0.f, 0.f}, b[4];
   if (n + 4 <= a.n) {
 #pragma unroll 8
-    for (int32_t k = 0; k < a.splits; ++k) {
+    for (int32_t k = 0; k < a.plan.splits; ++k) {
       float f[4];
       __builtin_memcpy(f, p + k * apart, 16);
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] += f[r];
     }
   } else {
-    for (int32_t k = 0; k < a.splits; ++k)
+    for (int32_t k = 0; k < a.plan.splits; ++k)
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] += n + r < a.n ? p[k * apart + r] : 0.f;
   }
@@ -466,192 +582,230 @@ __global__ __launch_bounds__(256) void f8_join_kernel(F8Args a) {
 // ---------------------------------------------------------------- few rows
 
 // Few tokens: the weights are read once, straight into the matrix instruction's registers.  A workgroup of 8 wavefronts
-// takes RT blocks of 16 weight rows (with the gate RT / 2 blocks of gate rows and as many of up rows) and up to 16 MT
-// tokens; its wavefronts cut K, their sums meet in LDS.  Two sets of U steps are in registers, one on its way while the
-// other is used; the steps of a last, partial set are loaded again from the last one and left out.
-// XT >= 0: the tokens come as they are and each wavefront cuts its own part of K to 8 bits, in LDS, while its first weights
-// are on their way: a block's scale needs no other wavefront, so there is no barrier and no launch in front.
-template <int RT, int MT, bool GATED, int XT>
-__global__ __launch_bounds__(512) void f8_few_kernel(F8Args a) {
+// takes groups of RT blocks of 16 weight rows (with the gate RT / 2 blocks of gate rows and as many of up rows) one after
+// the other, and 16 tokens at most; its wavefronts cut K, their sums meet in LDS.  Two sets of U steps are in registers, one
+// on its way while the other is used, across the groups: the first steps of the next group are asked for before the sums
+// of this one meet.  The steps of a last, partial set are the last one again and left out.
+// XT >= 0: the tokens come as they are and each wavefront cuts its own part of K to 8 bits, in LDS, once, while its first
+// weights are on their way: a block's scale needs no other wavefront, so there is no barrier and no launch in front.
+// SPLIT: workgroups cut K too (blockIdx.y), and their sums go to `part`.
+template <int RT, bool GATED, bool SPLIT, int XT>
+__global__ __launch_bounds__(512, 4) void f8_few_kernel(F8Args a, int32_t groups) {
   constexpr bool CUT = XT >= 0;
-  static_assert(!CUT || MT == 1, "tokens of one block");
-  static_assert(!GATED || RT % 2 == 0, "gate and up blocks");
+  static_assert(!GATED || (RT % 2 == 0 && !SPLIT), "gate and up blocks");
   constexpr int NO = GATED ? RT / 2 : RT;
-  constexpr int kTiles = RT * MT;
-  constexpr int U = kTiles == 1 ? 4 : kTiles <= 4 ? 2 : 1;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [8][kTiles][64] v4f, then the cut tokens
+  constexpr int U = CUT ? 4 / RT : 2 / RT;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [8][RT][64] v4f, then the cut tokens
+
+  // all arguments at once: each of their cache lines that is first read later would cost a small product half a microsecond
+  asm volatile("" ::"s"(a.w), "s"(a.sw), "s"(a.y), "s"(a.plan.splits), "s"(groups));
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, grp = lane >> 4;
-  const int32_t n0 = (int32_t)blockIdx.x * 16 * NO;
   const int64_t ld = vqi::q8_row_bytes(a.k);
-  const int32_t blocks = (int32_t)(ld / kStep);
-  const int32_t k0 = (int32_t)((int64_t)blocks * wave / 8), k1 = (int32_t)((int64_t)blocks * (wave + 1) / 8);
+  const int32_t blocks = (int32_t)(ld / kStep), nblocks = (int32_t)vqi::f8_blocks(a.n);
+  int32_t first = 0, last = blocks;
+  if constexpr (SPLIT) {
+    first = (int32_t)((int64_t)blocks * blockIdx.y / a.plan.splits);
+    last = (int32_t)((int64_t)blocks * (blockIdx.y + 1) / a.plan.splits);
+  }
+  const int32_t k0 = first + (last - first) * wave / 8, k1 = first + (last - first) * (wave + 1) / 8;
+  const int32_t sets = (k1 - k0 + U - 1) / U;  // of each group; a short K leaves wavefronts without any
+  const int32_t mine = min(row, a.m - 1);
   v4f* const red = (v4f*)lds;
 
-  v4f acc[RT][MT];
+  v4f acc[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < RT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  if (k0 < k1) {
-    const uint8_t* gw[RT];
+  // the tokens' part of this wavefront in pieces of 16 columns: piece e is piece e % pieces of token e / pieces, columns
+  // 16 (.. % 8) .. of step k0 + .. / 8.  The first ones are asked for before the weights, which then arrive behind them
+  constexpr vq_dtype XD = CUT ? (vq_dtype)XT : VQ_F32;
+  constexpr int kAhead = GATED || XT == VQ_F32 ? 1 : 2;  // what 128 registers hold
+  const int32_t pieces = (k1 - k0) * 8, all = pieces * a.m;
+  auto token_of = [&](int32_t e) { return a.m == 1 ? 0 : e / pieces; };  // one token: no division before its loads
+  auto piece = [&](int32_t e) {
+    const int32_t m = token_of(e), c = e - m * pieces;
+    return vqd::load_run<XD, 16>((const char*)a.x + (int64_t)m * a.ldx * (XD == VQ_F32 ? 4 : 2), k0 * kStep + c * 16, a.k);
+  };
+  vqd::Run<XD, 16> raw[CUT ? kAhead : 1];
+  if constexpr (CUT) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (lane + 64 * i < all) raw[i] = piece(lane + 64 * i);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  v4i w[2][U][RT][2], t[2][CUT ? 1 : U][2];
+  float ts[2][CUT ? 1 : U], sg[2], su[2];  // sg, su: the weights' scales of a set's steps, one per lane
+  const uint8_t* gw[RT];
+  const uint8_t* const gt = CUT ? nullptr : a.q + (int64_t)mine * ld + grp * 32;
+  const float* sw = nullptr;
+  int32_t ask_group = (int32_t)blockIdx.x, ask_set = 0;
+  auto ask = [&](int set) {  // the next set of steps, of this group or the next
+    if (ask_group >= groups) return;
+    if (ask_set == 0) {
+      const int32_t n0 = ask_group * 16 * NO;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int64_t r = (int64_t)min(n0 + 16 * (i % NO) + row, a.n - 1) + (i >= NO ? a.n : 0);
+        gw[i] = a.w + r * ld + grp * 32;
+      }
+      sw = a.sw + (int64_t)(n0 / 128) * blocks;
+    }
+    const int32_t at = k0 + ask_set * U;
+    sg[set] = sw[min(at + (lane & 3), k1 - 1)];
+    if constexpr (GATED) su[set] = sw[(int64_t)nblocks * blocks + min(at + (lane & 3), k1 - 1)];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t k = min(at + u, k1 - 1);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[set][u][i][h] = *(const v4i*)(gw[i] + (int64_t)k * kStep + 16 * h);
+      if constexpr (!CUT) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) t[set][u][h] = *(const v4i*)(gt + (int64_t)k * kStep + 16 * h);
+        ts[set][u] = a.s[(int64_t)k * a.m + mine];
+      }
+    }
+    if (++ask_set == sets) {
+      ask_set = 0;
+      ask_group += (int32_t)gridDim.x;
+    }
+  };
+  if (sets > 0) {
+    ask(0);
+    ask(1);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+
+  uint8_t* const xq = lds + 8 * RT * 1024 + (int64_t)(k0 - first) * a.m * (kStep + 4);  // [steps][m][128], [steps][m] scales
+  float* const xs = (float*)(xq + (int64_t)(k1 - k0) * a.m * kStep);
+  if constexpr (CUT) {
+    for (int32_t e0 = 0; e0 < all; e0 += 64 * kAhead) {
+      if (e0 > 0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (e0 + lane + 64 * i < all) raw[i] = piece(e0 + lane + 64 * i);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (e0 + 64 * i >= all) break;
+        const int32_t e = e0 + lane + 64 * i;
+        float f[16];
+        vqd::widen(raw[i], f);
+        uint32_t big = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) big = max(big, vqd::abs_bits(f[k]));
+        big = vqd::group_max<8>(big);
+        if (e < all) {  // 8 lanes at once
+          const int32_t m = token_of(e), c = e - m * pieces;
+          const vqd::Q8Scale sc = vqd::f8_scale(big);
+          const int32_t at = (c >> 3) * a.m + m;
+          *(uint4*)(xq + (int64_t)at * kStep + ((c & 7) ^ ((m >> 1) & 7)) * 16) =
+              make_uint4(vqd::f8_pack4(f, sc), vqd::f8_pack4(f + 4, sc), vqd::f8_pack4(f + 8, sc), vqd::f8_pack4(f + 12, sc));
+          if ((c & 7) == 0) xs[at] = sc.s;
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+
+  const int c0 = ((2 * grp) ^ ((mine >> 1) & 7)) * 16;
+  auto use = [&](int set, int32_t at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (at + u >= k1) break;
+      auto scale = [&](float v) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), u)); };
+      const float g = scale(sg[set]), h = GATED ? scale(su[set]) : 0.f;
+      Frag<true> tok;
+      float s;
+      if constexpr (CUT) {
+        const uint8_t* p = xq + (int64_t)((at + u - k0) * a.m + mine) * kStep;
+        tok = join<true>(*(const v4i*)(p + c0), *(const v4i*)(p + (c0 ^ 16)));
+        s = xs[(at + u - k0) * a.m + mine];
+      } else {
+        tok = join<true>(t[set][u][0], t[set][u][1]);
+        s = ts[set][u];
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const v4f p = multiply<true>(join<true>(w[set][u][i][0], w[set][u][i][1]), tok);
+        const float c = s * (GATED && i >= NO ? h : g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(p[r], c, acc[i][r]);
+      }
+    }
+  };
+  // The sums of a group meet and are stored.  The barriers are bare: loads stay on their way across them.
+  auto finish = [&](int32_t group) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the reads of the group before are done
+    meet();
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const int64_t r = (int64_t)min(n0 + 16 * (i % NO) + row, a.n - 1) + (i >= NO ? a.n : 0);
-      gw[i] = a.w + r * ld + grp * 16;
+      red[(wave * RT + i) * 64 + lane] = acc[i];
+      acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-    const uint8_t* gt[MT];
-    const float* gs[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int32_t m = min(16 * j + row, a.m - 1);
-      gt[j] = CUT ? nullptr : a.q + (int64_t)m * ld + grp * 16;
-      gs[j] = CUT ? nullptr : a.s + m;
-    }
-    // the weights' scales of this wavefront's steps (64 at most), one per lane
-    const int32_t nblocks = (int32_t)vqi::f8_blocks(a.n);
-    const float* sw = a.sw + (int64_t)(n0 / 128) * blocks + min(k0 + lane, k1 - 1);
-    const float sg = sw[0], su = GATED ? sw[(int64_t)nblocks * blocks] : 0.f;
-
-    // the tokens' part of this wavefront, in chunks of 16: chunk c is columns 16 (c % 8) .. of step k0 + c / 8
-    constexpr vq_dtype XD = CUT ? (vq_dtype)XT : VQ_F32;
-    const int32_t chunks = (k1 - k0) * 8;
-    float first[CUT ? 16 : 1];
-    if constexpr (CUT) {
-      // the first ones are asked for before the weights, which then arrive behind them
-      if (lane < chunks) vqd::load_f32<XD, 16>(a.x, k0 * kStep + lane * 16, a.k, first);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-
-    v4i w[2][U][RT][2], t[2][CUT ? 1 : U][MT][2];
-    float ts[2][CUT ? 1 : U][MT];
-    auto load = [&](int set, int32_t at) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int32_t k = min(at + u, k1 - 1);
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            w[set][u][i][h] = __builtin_nontemporal_load((const v4i*)(gw[i] + (int64_t)k * kStep + 64 * h));
-        if constexpr (!CUT) {
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) t[set][u][j][h] = *(const v4i*)(gt[j] + (int64_t)k * kStep + 64 * h);
-            ts[set][u][j] = gs[j][(int64_t)k * a.m];
-          }
-        }
-      }
-    };
-    const int32_t sets = (k1 - k0 + U - 1) / U;
-    load(0, k0);
-    if (sets > 1) load(1, k0 + U);
-    __builtin_amdgcn_sched_barrier(0);
-
-    uint8_t* const xq = lds + 8 * kTiles * 1024 + (int64_t)k0 * a.m * (kStep + 4);  // [steps][m][128], [steps][m] scales
-    float* const xs = (float*)(xq + (int64_t)(k1 - k0) * a.m * kStep);
-    if constexpr (CUT) {
-      for (int32_t m = 0; m < a.m; ++m) {
-        const void* x = (const char*)a.x + (int64_t)m * a.ldx * (XD == VQ_F32 ? 4 : 2);
-        for (int32_t c = lane; c < (chunks + 63) / 64 * 64; c += 64) {
-          float f[16];
-          if (m == 0 && c < 64) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = first[k];
-          } else if (c < chunks) {
-            vqd::load_f32<XD, 16>(x, k0 * kStep + c * 16, a.k, f);
-          }
-          uint32_t big = 0;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) big = max(big, vqd::abs_bits(f[k]));
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) big = max(big, (uint32_t)__shfl_xor((int)big, o, 64));
-          if (c < chunks) {  // 8 lanes at once
-            const vqd::Q8Scale sc = vqd::f8_scale(big);
-            const int32_t at = (c >> 3) * a.m + m;
-            *(uint4*)(xq + (int64_t)at * kStep + ((c & 7) ^ ((m >> 1) & 7)) * 16) =
-                make_uint4(vqd::f8_pack4(f, sc), vqd::f8_pack4(f + 4, sc), vqd::f8_pack4(f + 8, sc), vqd::f8_pack4(f + 12, sc));
-            if ((c & 7) == 0) xs[at] = sc.s;
-          }
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    }
-
-    const int32_t mine = min(row, a.m - 1);
-    const int c0 = (grp ^ ((mine >> 1) & 7)) * 16;
-    auto use = [&](int set, int32_t at) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (at + u >= k1) break;
-        const float g = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sg), at + u - k0));
-        const float h = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, su), at + u - k0)) : 0.f;
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          Frag<true> tok;
-          float s;
-          if constexpr (CUT) {
-            const uint8_t* p = xq + (int64_t)((at + u - k0) * a.m + mine) * kStep;
-            tok = join<true>(*(const v4i*)(p + c0), *(const v4i*)(p + (c0 ^ 64)));
-            s = xs[(at + u - k0) * a.m + mine];
-          } else {
-            tok = join<true>(t[set][u][j][0], t[set][u][j][1]);
-            s = ts[set][u][j];
-          }
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const v4f p = multiply<true>(join<true>(w[set][u][i][0], w[set][u][i][1]), tok);
-            const float c = s * (GATED && i >= NO ? h : g);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], c, acc[i][j][r]);
-          }
-        }
-      }
-    };
-    for (int32_t b = 0; b < sets; b += 2) {
-      use(0, k0 + b * U);
-      if (b + 2 < sets) load(0, k0 + (b + 2) * U);
-      if (b + 1 < sets) {
-        use(1, k0 + (b + 1) * U);
-        if (b + 3 < sets) load(1, k0 + (b + 3) * U);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) red[(wave * kTiles + i * MT + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-
-  // lane: token lane % 16, channels 4 (lane / 16) .. + 3 of a block; the wavefronts share the blocks out
-  for (int o = wave; o < NO * MT; o += 8) {
-    const int j = o % MT, i = o / MT;
-    const int32_t m = 16 * j + row;
-    const int32_t n = n0 + 16 * i + 4 * grp;
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    meet();
+    // lane: token lane % 16, channels 4 (lane / 16) .. + 3 of a block; a wavefront for each block
+    if (wave >= NO) return;
     auto total = [&](int at) {
       v4f sum = red[at * 64 + lane];
 #pragma unroll
-      for (int v = 1; v < 8; ++v) sum += red[(v * kTiles + at) * 64 + lane];
+      for (int v = 1; v < 8; ++v) sum += red[(v * RT + at) * 64 + lane];
       return sum;
     };
-    const v4f sum = total(o);
+    int32_t tok = row;
+    asm volatile("" : "+v"(tok));  // its addresses are formed here, not kept in registers from the start
+    const int32_t n = group * 16 * NO + 16 * wave + 4 * grp;
+    const v4f sum = total(wave);
     float v[4], b[4];
-    load_bias<4>(a.bias, n, a.n, b);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = sum[r] + b[r];
-    if constexpr (GATED) {
-      const v4f up = total(o + NO * MT);
-      load_bias<4>(a.bias ? a.bias + a.n : nullptr, n, a.n, b);
+    for (int r = 0; r < 4; ++r) v[r] = sum[r];
+    if constexpr (SPLIT) {
+      if (tok < a.m) store_run<4>(a.part, VQ_F32, ((int64_t)blockIdx.y * a.m + tok) * a.n, n, a.n, v);
+    } else {
+      if (a.bias) {
+        load_bias<4>(a.bias, n, a.n, b);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = silu(v[r]) * (up[r] + b[r]);
+        for (int r = 0; r < 4; ++r) v[r] += b[r];
+      }
+      if constexpr (GATED) {
+        v4f up = total(wave + NO);
+        if (a.bias) {
+          load_bias<4>(a.bias + a.n, n, a.n, b);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) up[r] += b[r];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = silu(v[r]) * up[r];
+      }
+      if (tok < a.m) store_run<4>(a.y, a.y_dtype, (int64_t)tok * a.n, n, a.n, v);
     }
-    if (m < a.m) store_run<4>(a.y, a.y_dtype, (int64_t)m * a.n, n, a.n, v);
+  };
+
+  int32_t group = (int32_t)blockIdx.x, at_set = 0;
+  auto turn = [&](int set) {
+    use(set, k0 + at_set * U);
+    ask(set);
+    if (++at_set == sets) {
+      finish(group);
+      at_set = 0;
+      group += (int32_t)gridDim.x;
+    }
+  };
+  if (sets == 0) {
+    for (; group < groups; group += (int32_t)gridDim.x) finish(group);
+  }
+  while (group < groups) {
+    turn(0);
+    if (group < groups) turn(1);
   }
 }
 
@@ -659,52 +813,58 @@ __global__ __launch_bounds__(512) void f8_few_kernel(F8Args a) {
 
 vq_status done() { return hipGetLastError() == hipSuccess ? VQ_OK : VQ_ERR_HIP; }
 
-// Blocks of 16 outputs per workgroup of the kernels that stream the weights: 4, 2 or 1, as many as leave most CUs a
-// workgroup (with the gate a block is 32 weight rows).
-inline int out_blocks(int32_t n, bool gated) {
-  if (gated) return n / 32 >= 192 ? 2 : 1;
-  return n / 64 >= 192 ? 4 : n / 32 > 144 ? 2 : 1;
-}
-
 constexpr size_t kCutLds = 64 * 1024;
-constexpr size_t few_lds(int tiles, int32_t m, int32_t k, bool cut) {
-  return (size_t)8 * tiles * 1024 + (cut ? (size_t)vqi::f8_blocks(k) * m * (kStep + 4) : 0);
+// Dynamic LDS of the streaming kernel: the wavefronts' sums, and the cut tokens of a workgroup's steps.
+constexpr size_t few_lds(int rt, int32_t m, int32_t steps, bool cut) {
+  return (size_t)8 * rt * 1024 + (cut ? (size_t)steps * m * (kStep + 4) : 0);
 }
 
-template <int RT, int MT, bool GATED, int XT>
+vq_status launch_join(const F8Args& a, hipStream_t st) {
+  const int64_t items = (int64_t)a.m * ((a.n + 3) / 4);  // K is cut for few tiles only: a small grid
+  f8_join_kernel<<<dim3((uint32_t)((items + 255) / 256)), dim3(256), 0, st>>>(a);
+  return done();
+}
+
+// Workgroups of the streaming kernel: as many as the CUs hold at once, two each.
+constexpr int32_t kFewWorkgroups = 512;
+
+template <int RT, bool GATED, int XT>
 vq_status few(const F8Args& a, hipStream_t st, bool check_only) {
   constexpr int out = (GATED ? RT / 2 : RT) * 16;
-  const int64_t blocks = ((int64_t)a.n + out - 1) / out;
-  if (!vqi::grid_ok(blocks, 512)) return VQ_ERR_SHAPE;
-  if (check_only) return VQ_OK;
-  f8_few_kernel<RT, MT, GATED, XT><<<dim3((uint32_t)blocks), dim3(512), few_lds(RT * MT, a.m, a.k, XT >= 0), st>>>(a);
+  if (check_only) return VQ_OK;  // a bounded grid
+  const int32_t groups = (int32_t)(((int64_t)a.n + out - 1) / out);
+  const size_t lds = few_lds(RT, a.m, (int32_t)((vqi::f8_blocks(a.k) + a.plan.splits - 1) / a.plan.splits), XT >= 0);
+  const dim3 g((uint32_t)std::min(groups, std::max(kFewWorkgroups / a.plan.splits, 1)), (uint32_t)a.plan.splits), b(512);
+  if constexpr (!GATED) {
+    if (a.plan.splits > 1) {
+      f8_few_kernel<RT, GATED, true, XT><<<g, b, lds, st>>>(a, groups);
+      const vq_status e = done();
+      return e != VQ_OK ? e : launch_join(a, st);
+    }
+  }
+  f8_few_kernel<RT, GATED, false, XT><<<g, b, lds, st>>>(a, groups);
   return done();
 }
 template <int RT, bool GATED>
 vq_status few_cut(const F8Args& a, hipStream_t st, bool check_only) {
   switch (a.x_dtype) {
-    case VQ_F32: return few<RT, 1, GATED, VQ_F32>(a, st, check_only);
-    case VQ_F16: return few<RT, 1, GATED, VQ_F16>(a, st, check_only);
-    default: return few<RT, 1, GATED, VQ_BF16>(a, st, check_only);
+    case VQ_F32: return few<RT, GATED, VQ_F32>(a, st, check_only);
+    case VQ_F16: return few<RT, GATED, VQ_F16>(a, st, check_only);
+    default: return few<RT, GATED, VQ_BF16>(a, st, check_only);
   }
 }
 
-template <int BM, int BN, int WM, int WN, int NB, bool WIDE, bool GATED, bool SPLIT>
+template <int BM, int BN, int WM, int WN, int NB, int KG, bool WIDE, bool GATED, bool SPLIT>
 vq_status launch_tile(const F8Args& a, hipStream_t st, bool check_only) {
   const int out = GATED ? BN / 2 : BN;
   const int64_t mt = ((int64_t)a.m + BM - 1) / BM;
   const int64_t nt = ((int64_t)a.n + out - 1) / out;
-  constexpr int kThreads = 64 * WM * WN;
+  constexpr int kThreads = 64 * WM * WN * KG;
   if (!vqi::grid_ok(mt * nt + 8, kThreads)) return VQ_ERR_SHAPE;
   if (check_only) return VQ_OK;
   const uint32_t blocks = (uint32_t)((mt * nt + 7) / 8 * 8);
-  f8_tile_kernel<BM, BN, WM, WN, NB, WIDE, GATED, SPLIT>
-      <<<dim3(blocks, SPLIT ? a.splits : 1), dim3(kThreads), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
-  return done();
-}
-vq_status launch_join(const F8Args& a, hipStream_t st) {
-  const int64_t items = (int64_t)a.m * ((a.n + 3) / 4);  // few tiles: a small grid
-  f8_join_kernel<<<dim3((uint32_t)((items + 255) / 256)), dim3(256), 0, st>>>(a);
+  f8_tile_kernel<BM, BN, WM, WN, NB, KG, WIDE, GATED, SPLIT>
+      <<<dim3(blocks, SPLIT ? a.plan.splits : 1), dim3(kThreads), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
   return done();
 }
 template <bool WIDE, bool GATED, bool OUTQ>
@@ -719,22 +879,134 @@ vq_status launch_big(const F8Args& a, hipStream_t st, bool check_only) {
   return done();
 }
 
-// How a product is computed.
-enum Way { kStreamed, k64x64, k128x128, k256x256 };
-struct Plan {
-  Way way;
-  int32_t splits;  // cuts of K over the CUs
+// ---------------------------------------------------------------- which way
+
+// A way of computing a product and what it takes, in us: `start` for the launch and its ends, and for each round over the
+// CUs `round` and then `step` for each step of K, the first of them with one workgroup on a CU, then two and three, as many
+// as `together` (the LDS) says.  Fitted to 670 shapes from 1 to 4096 rows by 64 to 28672 columns and outputs, with weights
+// from memory, where they meet what was measured to 11 - 16 % (rms); the way with the least of these times, of a copy of the
+// operands and of the join of a cut K is taken.  Over those shapes that is 1.8 % slower than the best way of each (geometric
+// mean; at the worst 33 %, 15 and 20 us).  us, in the way that is taken and in the next ones:
+//   16-bit outputs: 37 x 5003 x 4099 11.4 in 32 x 32, 13.4 in 64 x 64, 14.6 in 64 x 128 / 4; 256 x 4096 x 4096 13.5 in
+//     64 x 64, 16.3 in 32 x 64, 19.6 in 128 x 64; 512 x 4096 x 4096 18.9 in 64 x 128, 24.4 in 128 x 128, 24.6 in 64 x 64;
+//     128 x 28672 x 8192 57.5 in 128 x 128, 64.8 in pairs of them, 68.3 in 64 x 128; 128 x 8192 x 28672 63 in 128 x 128 / 4,
+//     70.3 / 3, 72 in 64 x 128 / 2; 512 x 14336 x 4096 41.3 in pairs of 128 x 128, 49 in 256 x 256, 55.7 in 64 x 128;
+//     4096 x 14336 x 4096 232 in 256 x 256, 268 in pairs of 128 x 128
+//   fp32: 512 x 4096 x 4096 27.7 in 64 x 128, 32 in 64 x 64, 41 in 128 x 128; 4096 x 14336 x 4096 457 in pairs of 128 x 128,
+//     528 in 64 x 128 with four wavefronts
+//   few rows, streamed and in tiles, tokens in 8 bits: 16 x 4096 x 4096 7.1 and 9.3; 8 x 28672 x 8192 53 and 46.7; cut
+//     inside: 4 x 4096 x 4096 8.4, 3.3 + 6.3 otherwise; 8 x 4096 x 4096 10.2, 3.3 + 6.4
+enum Way : int32_t { kStream1, kStream2, k32x32, k32x64, k64x64, k64x128, k128x128, k128x128Pair, k256x256, kWays };
+struct Cost {
+  int32_t bm, bm_log2, bn, bn_log2, groups_of_k, together;
+  float start, round, step[3];
 };
-Plan plan(int32_t m, int32_t n, int32_t k, bool gated) {
-  const int64_t steps = vqi::f8_blocks(k);
-  if (m <= 16) return {kStreamed, 1};
-  auto tiles = [&](int bm, int bn) { return (((int64_t)m + bm - 1) / bm) * (((int64_t)n + bn - 1) / bn); };
-  auto cut = [&](int64_t t) {
-    return steps < 56 || gated ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / t, steps / 8));
-  };
-  if (tiles(256, gated ? 128 : 256) >= 200) return {k256x256, 1};
-  if (m <= 64) return {k64x64, cut(tiles(64, 64))};
-  return {k128x128, cut(tiles(128, 128))};
+constexpr Cost kCosts[2][kWays] = {
+    {{16, 4, 16, 4, 8, 2, 2.20f, 0.f, {0.85f, 1.74f}},
+     {16, 4, 32, 5, 8, 2, 1.83f, 0.f, {1.38f, 2.62f}},
+     {32, 5, 32, 5, 2, 2, 1.42f, 1.58f, {0.32f, 0.51f}},
+     {32, 5, 64, 6, 1, 3, 1.75f, 1.74f, {0.27f, 0.41f, 0.51f}},
+     {64, 6, 64, 6, 2, 1, 0.66f, 2.63f, {0.54f}},
+     {64, 6, 128, 7, 1, 2, 1.33f, 2.49f, {0.45f, 0.84f}},
+     {128, 7, 128, 7, 1, 1, 2.20f, 3.48f, {0.62f}},
+     {128, 7, 128, 7, 1, 2, 2.04f, 4.04f, {0.72f, 1.09f}},
+     {256, 8, 256, 8, 1, 1, 2.87f, 8.20f, {1.73f}}},
+    // operands in fp16
+    {{16, 4, 16, 4, 8, 2, 2.20f, 0.f, {0.85f, 1.74f}},
+     {16, 4, 32, 5, 8, 2, 1.83f, 0.f, {1.38f, 2.62f}},
+     {32, 5, 32, 5, 2, 2, 1.28f, 1.72f, {0.40f, 0.64f}},
+     {32, 5, 64, 6, 1, 3, 0.66f, 2.68f, {0.36f, 0.62f, 0.65f}},
+     {64, 6, 64, 6, 2, 1, 0.66f, 2.67f, {0.77f}},
+     {64, 6, 128, 7, 1, 2, 0.00f, 3.64f, {0.71f, 1.52f}},
+     {128, 7, 128, 7, 1, 1, 1.31f, 3.83f, {1.08f}},
+     {128, 7, 128, 7, 1, 2, 1.73f, 4.57f, {1.13f, 1.88f}},
+     {128, 7, 256, 8, 1, 1, 0.92f, 5.69f, {1.75f}}}};  // only where it writes its outputs in 8 bits
+// Cutting tokens to 8 bits: inside the streaming kernel (its start, and for each 64 pieces of 16 columns of a wavefront),
+// and in a launch of its own (and its bytes per us).
+constexpr float kCutStart[2] = {1.3f, 1.4f}, kCutPiece = 0.9f, kQuantStart = 3.3f, kQuantRate = 4e6f;
+constexpr float kCopyRate = 5.3e6f, kCopyStart = 2.0f;   // bytes per us of a large copy
+constexpr float kJoinStart = 2.6f, kJoinRate = 4.5e6f;   // the launch that adds up a cut K
+
+int32_t ceil_div(int32_t a, int32_t b) { return (int32_t)(((uint32_t)a + (uint32_t)b - 1) / (uint32_t)b); }
+
+// The parts of a product's cost that no way changes.
+struct Shape {
+  int32_t m, steps;
+  int64_t outputs;  // weight rows
+  float copy, out, parts;
+  Shape(int32_t m_, int32_t n, int32_t k, bool gated, bool wide)
+      : m(m_), steps((int32_t)vqi::f8_blocks(k)), outputs((int64_t)n * (gated ? 2 : 1)) {
+    out = (float)m * (float)n * (wide ? 4.f : 2.f);
+    parts = 8.f * (float)m * (float)n;
+    copy = kCopyStart + ((float)outputs * (float)k + (float)m * (float)k + out) / kCopyRate;
+  }
+};
+float cost(const Shape& s, int32_t way, int32_t splits, bool cut, bool wide) {
+  const Cost& c = kCosts[wide][way];
+  const float steps = (float)ceil_div(splits == 1 ? s.steps : ceil_div(s.steps, splits), c.groups_of_k);
+  const int32_t columns = (int32_t)((s.outputs + c.bn - 1) >> c.bn_log2);
+  float t = c.start;
+  if (way <= kStream2) {
+    // two workgroups on each CU, that take turns with the memory: parts of a round count as such
+    const float rounds = (float)columns * (float)splits * (1.f / kFewWorkgroups);
+    t += steps * (rounds <= 0.5f ? c.step[0] : c.step[1] * std::max(rounds, 1.f));
+    if (cut) t += kCutStart[way] + kCutPiece * 0.125f * (float)s.m * steps;
+  } else {
+    const int32_t rows = (int32_t)(((int64_t)s.m + c.bm - 1) >> c.bm_log2);
+    const int64_t tiles = (int64_t)rows * columns * splits;
+    if (way == k256x256 && !wide) {  // the last round in half tiles
+      const int32_t rest = (int32_t)(tiles & 255);
+      const float rounds = (float)(tiles >> 8) + (rest == 0 ? 0.f : rest <= 128 ? 0.55f : 1.f);
+      t += rounds * (c.round + steps * c.step[0]);
+    } else if (c.together == 1) {
+      t += (float)((tiles + 255) >> 8) * (c.round + steps * c.step[0]);
+    } else {
+      const uint64_t per_cu = (uint64_t)(tiles + 255) >> 8, full = per_cu / c.together, rest = per_cu - full * c.together;
+      t += (float)(full + (rest != 0)) * c.round + steps * (float)full * c.step[c.together - 1];
+      if (rest) t += steps * c.step[rest - 1];
+    }
+  }
+  t = std::max(t, s.copy);
+  if (splits > 1) t += kJoinStart + ((float)splits * s.parts + s.out) / kJoinRate;
+  return t;
+}
+
+vq_status stream(const F8Args& a, hipStream_t st, bool check_only) {
+  const bool two = a.plan.way == kStream2;
+  if (a.gated) return a.plan.cut ? few_cut<2, true>(a, st, check_only) : few<2, true, -1>(a, st, check_only);
+  if (two) return a.plan.cut ? few_cut<2, false>(a, st, check_only) : few<2, false, -1>(a, st, check_only);
+  return a.plan.cut ? few_cut<1, false>(a, st, check_only) : few<1, false, -1>(a, st, check_only);
+}
+
+template <int BM, int BN, int WM, int WN, int NB, int KG, bool WIDE>
+vq_status tiles(const F8Args& a, hipStream_t st, bool check_only) {
+  if (a.gated) return launch_tile<BM, BN, WM, WN, NB, KG, WIDE, true, false>(a, st, check_only);
+  if constexpr (KG == 1) {
+    if (a.plan.splits > 1) {
+      const vq_status e = launch_tile<BM, BN, WM, WN, NB, KG, WIDE, false, true>(a, st, check_only);
+      return e != VQ_OK || check_only ? e : launch_join(a, st);
+    }
+  }
+  return launch_tile<BM, BN, WM, WN, NB, KG, WIDE, false, false>(a, st, check_only);
+}
+template <bool WIDE>
+vq_status run(const F8Args& a, hipStream_t st, bool check_only) {
+  switch (a.plan.way) {
+    case kStream1:
+    case kStream2: return stream(a, st, check_only);
+    case k32x32: return tiles<32, 32, 2, 1, 4, 2, WIDE>(a, st, check_only);
+    case k32x64: return tiles<32, 64, 2, 2, 4, 1, WIDE>(a, st, check_only);
+    case k64x64: return tiles<64, 64, 2, 2, 3, 2, WIDE>(a, st, check_only);
+    case k64x128: return tiles<64, 128, 2, 4, 3, 1, WIDE>(a, st, check_only);
+    case k128x128: return tiles<128, 128, 4, 2, 3, 1, WIDE>(a, st, check_only);
+    case k128x128Pair: return tiles<128, 128, 2, 2, 2, 1, WIDE>(a, st, check_only);
+    default:
+      if (!a.y) return launch_big<WIDE, true, true>(a, st, check_only);
+      if constexpr (!WIDE) {
+        return a.gated ? launch_big<false, true, false>(a, st, check_only) : launch_big<false, false, false>(a, st, check_only);
+      }
+      return VQ_ERR_UNSUPPORTED;  // no plan has it
+  }
 }
 
 }  // namespace
@@ -768,50 +1040,56 @@ vq_status launch_f8_weights(const F8QuantArgs& a, void* stream) {
   return done();
 }
 
-int32_t f8_splits(int32_t m, int32_t n, int32_t k, bool gated) { return plan(m, n, k, gated).splits; }
-
-bool f8_cuts_inside(int32_t m, int32_t n, int32_t k, bool gated) {
-  const int tiles = out_blocks(n, gated) * (gated ? 2 : 1);
-  return m <= 4 && plan(m, n, k, gated).way == kStreamed && few_lds(tiles, m, k, true) <= kCutLds;
+F8Plan f8_plan(int32_t m, int32_t n, int32_t k, bool gated, bool wide, bool may_cut) {
+  const Shape shape(m, n, k, gated, wide);
+  const int32_t steps = shape.steps;
+  F8Plan best{-1, 1, false};
+  float least = 0.f;
+  const float quant = may_cut ? kQuantStart + 3.f * (float)m * (float)k / kQuantRate : 0.f;
+  auto offer = [&](int32_t way, int32_t splits, bool cut) {
+    const float t = cost(shape, way, splits, cut, wide) + (cut ? 0.f : quant);
+    if (best.way < 0 || t < least) {
+      least = t;
+      best = F8Plan{way, splits, cut};
+    }
+  };
+  for (int32_t way = 0; way < kWays; ++way) {
+    const Cost& c = kCosts[wide][way];
+    if (way <= kStream2) {
+      if (m > 16 || (gated && way == kStream1)) continue;
+      const int64_t groups = (shape.outputs + c.bn - 1) >> c.bn_log2;
+      for (int32_t z = 1; z <= 16; z *= 2) {
+        if (z > 1 && (gated || groups * z > kFewWorkgroups || steps / z < 8)) break;
+        offer(way, z, false);
+        if (may_cut && few_lds(way + 1, m, ceil_div(steps, z), true) <= kCutLds) offer(way, z, true);
+      }
+      continue;
+    }
+    if ((way == k256x256 && wide) || (c.bm > 64 && m <= 32)) continue;  // f8_big_plan; mostly empty tiles
+    offer(way, 1, false);
+    if (gated || c.groups_of_k > 1 || way == k256x256) continue;
+    // K is cut where the tiles leave CUs without work, into four steps at least
+    const int64_t t = (((int64_t)m + c.bm - 1) >> c.bm_log2) * ((shape.outputs + c.bn - 1) >> c.bn_log2);
+    for (const int32_t z : {2, 3, 4, 6, 8, 12, 16}) {
+      if (t * z > 300 || steps < 4 * z) break;
+      offer(way, z, false);
+    }
+  }
+  return best;
 }
 
-bool f8_writes_q(int32_t m, int32_t n, int32_t k) { return plan(m, n, k, true).way == k256x256; }
+bool f8_big_plan(int32_t m, int32_t n, int32_t k, bool wide, F8Plan& plan) {
+  // what the hidden rows cost otherwise: written and read in fp32, written in 8 bits, in a launch of their own
+  const float spared = kQuantStart + 9.f * (float)m * (float)n / kQuantRate;
+  const Shape s(m, n, k, true, wide);
+  if (cost(s, k256x256, 1, false, wide) > cost(s, plan.way, plan.splits, plan.cut, wide) + spared) return false;
+  plan = F8Plan{k256x256, 1, false};
+  return true;
+}
 
 vq_status launch_f8(const F8Args& a, void* stream, bool check_only) {
   hipStream_t st = (hipStream_t)stream;
-  const Plan p = plan(a.m, a.n, a.k, a.gated);
-  if (a.gated) {
-    switch (p.way) {
-      case kStreamed:
-        if (!a.q) return out_blocks(a.n, true) == 2 ? few_cut<4, true>(a, st, check_only) : few_cut<2, true>(a, st, check_only);
-        return out_blocks(a.n, true) == 2 ? few<4, 1, true, -1>(a, st, check_only) : few<2, 1, true, -1>(a, st, check_only);
-      case k64x64: return launch_tile<64, 128, 2, 2, 2, true, true, false>(a, st, check_only);
-      case k128x128: return launch_tile<128, 128, 2, 2, 2, true, true, false>(a, st, check_only);
-      default:
-        if (a.wide) return a.y ? launch_big<true, true, false>(a, st, check_only) : launch_big<true, true, true>(a, st, check_only);
-        return a.y ? launch_big<false, true, false>(a, st, check_only) : launch_big<false, true, true>(a, st, check_only);
-    }
-  }
-  switch (p.way) {
-    case kStreamed:
-      switch (out_blocks(a.n, false)) {
-        case 4: return a.q ? few<4, 1, false, -1>(a, st, check_only) : few_cut<4, false>(a, st, check_only);
-        case 2: return a.q ? few<2, 1, false, -1>(a, st, check_only) : few_cut<2, false>(a, st, check_only);
-        default: return a.q ? few<1, 1, false, -1>(a, st, check_only) : few_cut<1, false>(a, st, check_only);
-      }
-    case k64x64: {
-      if (a.splits == 1) return launch_tile<64, 64, 2, 2, 4, true, false, false>(a, st, check_only);
-      const vq_status e = launch_tile<64, 64, 2, 2, 4, true, false, true>(a, st, check_only);
-      return e != VQ_OK || check_only ? e : launch_join(a, st);
-    }
-    case k128x128: {
-      if (a.splits == 1) return launch_tile<128, 128, 2, 2, 2, true, false, false>(a, st, check_only);
-      const vq_status e = launch_tile<128, 128, 2, 2, 2, true, false, true>(a, st, check_only);
-      return e != VQ_OK || check_only ? e : launch_join(a, st);
-    }
-    case k256x256: return a.wide ? launch_big<true, false, false>(a, st, check_only) : launch_big<false, false, false>(a, st, check_only);
-  }
-  return VQ_ERR_UNSUPPORTED;
+  return a.wide ? run<true>(a, st, check_only) : run<false>(a, st, check_only);
 }
 
 }  // namespace vqi

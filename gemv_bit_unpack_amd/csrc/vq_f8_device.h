@@ -10,6 +10,24 @@
 
 namespace vqd {
 
+// The value of another lane of the 16-lane row, without LDS.  Where all lanes of a group of 2, 4 and 8 already hold the same,
+// kXor1, kXor2, kHalf and kRow one after the other bring in the rest of 2, 4, 8 and 16 consecutive lanes.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalf = 0x141, kRow = 0x140;
+template <int CTRL>
+__device__ __forceinline__ uint32_t other(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+// The largest of 8 (16) consecutive lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  static_assert(LANES == 8 || LANES == 16, "half a row or a row");
+  v = max(v, other<kXor1>(v));
+  v = max(v, other<kXor2>(v));
+  v = max(v, other<kHalf>(v));
+  if constexpr (LANES == 16) v = max(v, other<kRow>(v));
+  return v;
+}
+
 constexpr float kF8Top = 448.0f;  // the largest e4m3 value
 
 // The scale of a block whose largest |x| has the bits `big`: s = max|x| / 448, and what its quotients need (as Q8Scale
@@ -41,33 +59,44 @@ __device__ __forceinline__ uint32_t f8_pack4(const float* f, const Q8Scale& c) {
   return (uint32_t)w;
 }
 
-// Elements at .. at + CNT - 1 of a row that ends before element `end`, as fp32; zeros from there on.
+// Elements at .. at + CNT - 1 of a row of `end` elements, as they are; zeros from its end on.  Nothing outside the row is
+// read: where it ends inside, every word is loaded from no further than its last two elements (one for fp32), all of them
+// together, and shifted or cleared afterwards.
 template <vq_dtype XT, int CNT>
-__device__ __forceinline__ void load_f32(const void* row, int32_t at, int32_t end, float (&f)[CNT]) {
-  constexpr int es = XT == VQ_F32 ? 4 : 2;
-  const char* p = (const char*)row + (int64_t)at * es;
+struct Run {
+  uint32_t v[CNT * (XT == VQ_F32 ? 4 : 2) / 4];
+};
+template <vq_dtype XT, int CNT>
+__device__ __forceinline__ Run<XT, CNT> load_run(const void* row, int32_t at, int32_t end) {
+  constexpr int es = XT == VQ_F32 ? 4 : 2, per = 4 / es;  // elements of a word
+  Run<XT, CNT> r;
   if (at + CNT <= end) {
-    uint32_t v[CNT * es / 4];
-    __builtin_memcpy(v, p, CNT * es);
+    __builtin_memcpy(r.v, (const char*)row + (int64_t)at * es, CNT * es);
+  } else if (end >= per) {
 #pragma unroll
-    for (int k = 0; k < CNT; ++k) {
-      if constexpr (XT == VQ_F32) {
-        f[k] = __builtin_bit_cast(float, v[k]);
-      } else {
-        f[k] = x_to_f32<XT == VQ_F16 ? 0 : 1>(v[k / 2] >> (16 * (k & 1)));
-      }
+    for (int k = 0; k < CNT / per; ++k)
+      __builtin_memcpy(&r.v[k], (const char*)row + (int64_t)min(at + k * per, end - per) * es, 4);
+#pragma unroll
+    for (int k = 0; k < CNT / per; ++k) {
+      const int32_t e = at + k * per;
+      if (per == 2 && e == end - 1) r.v[k] >>= 16;
+      if (e >= end) r.v[k] = 0;
     }
-  } else {
+  } else {  // a single 16-bit element
 #pragma unroll
-    for (int k = 0; k < CNT; ++k) {
-      f[k] = 0.f;
-      if (at + k < end) {
-        if constexpr (XT == VQ_F32) {
-          f[k] = ((const float*)p)[k];
-        } else {
-          f[k] = x_to_f32<XT == VQ_F16 ? 0 : 1>(((const uint16_t*)p)[k]);
-        }
-      }
+    for (int k = 0; k < CNT / per; ++k) r.v[k] = 0;
+    if (at == 0 && end > 0) r.v[0] = *(const uint16_t*)row;
+  }
+  return r;
+}
+template <vq_dtype XT, int CNT>
+__device__ __forceinline__ void widen(const Run<XT, CNT>& r, float (&f)[CNT]) {
+#pragma unroll
+  for (int k = 0; k < CNT; ++k) {
+    if constexpr (XT == VQ_F32) {
+      f[k] = __builtin_bit_cast(float, r.v[k]);
+    } else {
+      f[k] = x_to_f32<XT == VQ_F16 ? 0 : 1>(r.v[k / 2] >> (16 * (k & 1)));
     }
   }
 }

@@ -15,50 +15,78 @@ vq_status check_sizes(int32_t M, int32_t N, int32_t K, int32_t gated) {
   return gated == 0 || gated == 1 ? VQ_OK : VQ_ERR_UNSUPPORTED;
 }
 
-size_t part_bytes(int32_t m, int32_t n, int32_t k, bool gated, int32_t* splits) {
-  *splits = m > 0 && n > 0 ? f8_splits(m, n, k, gated) : 1;
-  return *splits > 1 ? (size_t)*splits * (size_t)m * (size_t)n * 4 : 0;
+size_t part_bytes(int32_t m, int32_t n, const F8Plan& p) { return p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)n * 4 : 0; }
+
+// Most partial sums of a product of this shape, whatever the type of its outputs.
+size_t most_part_bytes(int32_t m, int32_t n, int32_t k, bool gated) {
+  if (m == 0 || n == 0) return 0;
+  return std::max(part_bytes(m, n, f8_plan(m, n, k, gated, false, false)), part_bytes(m, n, f8_plan(m, n, k, gated, true, false)));
 }
 
-// Tokens in 8 bits (if the product does not cut them itself) and a product's partial sums.
+// A product of tokens that are cut to 8 bits on the way: inside it, or in front of it, into q and s; and its partial sums.
 struct LinearWs {
+  F8Plan plan;
   uint8_t* q;
   float* s;
   float* part;
-  int32_t splits;
-  bool inside;
   size_t bytes;
 };
-LinearWs linear_ws(int32_t m, int32_t n, int32_t k, bool gated, void* base) {
+LinearWs linear_ws(int32_t m, int32_t n, int32_t k, bool gated, bool wide, void* base) {
   LinearWs w;
+  std::memset(&w, 0, sizeof w);
+  if (m == 0 || n == 0) return w;
+  w.plan = f8_plan(m, n, k, gated, wide, true);
   Pieces p{(uint8_t*)base};
-  w.inside = m > 0 && n > 0 && f8_cuts_inside(m, n, k, gated);
-  w.q = (uint8_t*)p.take(w.inside ? 0 : (size_t)m * (size_t)q8_row_bytes(k));
-  w.s = (float*)p.take(w.inside ? 0 : (size_t)m * (size_t)f8_blocks(k) * 4);
-  w.part = (float*)p.take(part_bytes(m, n, k, gated, &w.splits));
-  w.bytes = m > 0 && n > 0 ? p.at : 0;
+  w.q = (uint8_t*)p.take(w.plan.cut ? 0 : (size_t)m * (size_t)q8_row_bytes(k));
+  w.s = (float*)p.take(w.plan.cut ? 0 : (size_t)m * (size_t)f8_blocks(k) * 4);
+  w.part = (float*)p.take(part_bytes(m, n, w.plan));
+  w.bytes = p.at;
   return w;
+}
+size_t most_linear_bytes(int32_t m, int32_t n, int32_t k, bool gated) {
+  return std::max(linear_ws(m, n, k, gated, false, nullptr).bytes, linear_ws(m, n, k, gated, true, nullptr).bytes);
 }
 
 // Between the two products of an MLP: the hidden rows in fp32, or in 8 bits where the first product writes them so; and
-// one piece that both products use in turn.
+// one piece that both products use in turn.  The hidden rows are cut to 8 bits with sums as exact as the outputs can show:
+// a bf16 output's half step hides those that the 8-bit instruction moves to the next value, an fp16 output's does not.
 struct MlpWs {
+  bool wide_in, writes_q;
   float* h;
   uint8_t* hq;
   float* hs;
-  void* products;
-  bool writes_q;
+  LinearWs in, out;
   size_t bytes;
 };
-MlpWs mlp_ws(int32_t m, int32_t d, int32_t i, void* base) {
+MlpWs mlp_ws(int32_t m, int32_t d, int32_t i, vq_dtype y_dtype, void* base) {
   MlpWs w;
+  std::memset(&w, 0, sizeof w);
+  if (m == 0) return w;
+  w.wide_in = y_dtype != VQ_BF16;
+  w.in = linear_ws(m, i, d, true, w.wide_in, nullptr);
+  w.out = linear_ws(m, d, i, false, y_dtype == VQ_F32, nullptr);
+  F8Plan big = w.in.plan;
+  w.writes_q = f8_big_plan(m, i, d, w.wide_in, big);
   Pieces p{(uint8_t*)base};
-  w.writes_q = m > 0 && f8_writes_q(m, i, d);
   w.h = (float*)p.take(w.writes_q ? 0 : (size_t)m * (size_t)i * 4);
   w.hq = (uint8_t*)p.take(w.writes_q ? (size_t)m * (size_t)q8_row_bytes(i) : 0);
   w.hs = (float*)p.take(w.writes_q ? (size_t)m * (size_t)f8_blocks(i) * 4 : 0);
-  w.products = p.take(std::max(linear_ws(m, i, d, true, nullptr).bytes, linear_ws(m, d, i, false, nullptr).bytes));
-  w.bytes = m > 0 ? p.at : 0;
+  if (w.writes_q) {
+    w.in.plan = big;  // its tokens are cut in front of it
+    w.in.bytes = padded((size_t)m * (size_t)q8_row_bytes(d)) + padded((size_t)m * (size_t)f8_blocks(d) * 4);
+    w.out.plan = f8_plan(m, d, i, false, y_dtype == VQ_F32, false);
+    w.out.bytes = padded(part_bytes(m, d, w.out.plan));
+  }
+  void* const products = p.take(std::max(w.in.bytes, w.out.bytes));
+  auto place = [&](LinearWs& l, int32_t k, int32_t n, bool tokens) {
+    Pieces at{(uint8_t*)products};
+    l.q = (uint8_t*)at.take(tokens ? (size_t)m * (size_t)q8_row_bytes(k) : 0);
+    l.s = (float*)at.take(tokens ? (size_t)m * (size_t)f8_blocks(k) * 4 : 0);
+    l.part = (float*)at.take(part_bytes(m, n, l.plan));
+  };
+  place(w.in, d, i, !w.in.plan.cut);
+  place(w.out, i, d, !w.out.plan.cut && !w.writes_q);
+  w.bytes = p.at;
   return w;
 }
 
@@ -90,13 +118,14 @@ F8Args product(int32_t m, int32_t n, int32_t k, const void* w, const float* sw, 
   a.y = y;
   a.y_dtype = y_dtype;
   a.wide = y_dtype == VQ_F32;
-  a.splits = 1;
   return a;
 }
 
 // The product `a` of tokens x [m][k] that are cut to 8 bits on the way.
 vq_status linear(F8Args a, const void* x, vq_dtype x_dtype, int64_t ldx, const LinearWs& ws, void* stream, bool check_only) {
-  if (ws.inside) {
+  a.plan = ws.plan;
+  a.part = ws.part;
+  if (a.plan.cut) {
     a.x = x;
     a.x_dtype = x_dtype;
     a.ldx = ldx;
@@ -105,8 +134,6 @@ vq_status linear(F8Args a, const void* x, vq_dtype x_dtype, int64_t ldx, const L
     if (st != VQ_OK) return st;
     a.q = ws.q;
     a.s = ws.s;
-    a.splits = ws.splits;
-    a.part = ws.part;
   }
   return launch_f8(a, stream, check_only);
 }
@@ -142,8 +169,7 @@ vq_status vq_f8_gemm_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t ga
   if (!nbytes) return VQ_ERR_NULL;
   const vq_status st = check_sizes(M, N, K, gated);
   if (st != VQ_OK) return st;
-  int32_t splits;
-  *nbytes = part_bytes(M, N, K, gated, &splits);
+  *nbytes = most_part_bytes(M, N, K, gated);
   return VQ_OK;
 }
 
@@ -161,13 +187,13 @@ vq_status vq_f8_gemm(int32_t M, int32_t N, int32_t K, const void* q, const float
   F8Args a = product(M, N, K, w, sw, bias, gated, y, y_dtype);
   a.q = (const uint8_t*)q;
   a.s = s;
-  const size_t need = part_bytes(M, N, K, gated, &a.splits);
-  if (workspace && need > 0) {
-    if (workspace_bytes < need) return VQ_ERR_BUFFER_SIZE;
+  a.plan = f8_plan(M, N, K, gated, a.wide, false);
+  if (workspace && a.plan.splits > 1) {
+    if (workspace_bytes < part_bytes(M, N, a.plan)) return VQ_ERR_BUFFER_SIZE;
     if (!aligned(workspace, 256)) return VQ_ERR_ALIGN;
     a.part = (float*)workspace;
   } else {
-    a.splits = 1;
+    a.plan.splits = 1;
   }
   return launch_f8(a, stream);
 }
@@ -176,7 +202,7 @@ vq_status vq_f8_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t 
   if (!nbytes) return VQ_ERR_NULL;
   const vq_status st = check_sizes(M, N, K, gated);
   if (st != VQ_OK) return st;
-  *nbytes = linear_ws(M, N, K, gated, nullptr).bytes;
+  *nbytes = most_linear_bytes(M, N, K, gated);
   return VQ_OK;
 }
 
@@ -188,7 +214,7 @@ vq_status vq_f8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype 
   if (ldx < K) return VQ_ERR_SHAPE;
   if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype)) return VQ_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return VQ_OK;
-  const LinearWs ws = linear_ws(M, N, K, gated, workspace);
+  const LinearWs ws = linear_ws(M, N, K, gated, y_dtype == VQ_F32, workspace);
   if (!x || !w || !sw || !y || (!workspace && ws.bytes > 0)) return VQ_ERR_NULL;
   if (!aligned(x, size_of(x_dtype)) || !aligned(w, 16) || !aligned(sw, 4) || misaligned(bias, 2) ||
       !aligned(y, size_of(y_dtype)) || misaligned(workspace, 256))
@@ -202,7 +228,8 @@ vq_status vq_f8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype 
 vq_status vq_f8_mlp_workspace_bytes(int32_t M, int32_t D, int32_t I, size_t* nbytes) {
   if (!nbytes) return VQ_ERR_NULL;
   if (M < 0 || !valid_k(D) || !valid_k(I)) return VQ_ERR_SHAPE;
-  *nbytes = mlp_ws(M, D, I, nullptr).bytes;
+  *nbytes = 0;
+  for (const vq_dtype t : {VQ_F16, VQ_BF16, VQ_F32}) *nbytes = std::max(*nbytes, mlp_ws(M, D, I, t, nullptr).bytes);
   return VQ_OK;
 }
 
@@ -216,23 +243,22 @@ vq_status vq_f8_mlp(int32_t M, int32_t D, int32_t I, const void* x, vq_dtype x_d
   if (!aligned(x, size_of(x_dtype)) || !aligned(w_in, 16) || !aligned(w_out, 16) || !aligned(s_in, 4) ||
       !aligned(s_out, 4) || !aligned(y, size_of(y_dtype)) || !aligned(workspace, 256))
     return VQ_ERR_ALIGN;
-  const MlpWs ws = mlp_ws(M, D, I, workspace);
+  const MlpWs ws = mlp_ws(M, D, I, y_dtype, workspace);
   if (workspace_bytes < ws.bytes) return VQ_ERR_BUFFER_SIZE;
-  const LinearWs in = linear_ws(M, I, D, true, ws.products), out = linear_ws(M, D, I, false, ws.products);
   F8Args gate = product(M, I, D, w_in, s_in, nullptr, 1, ws.writes_q ? nullptr : ws.h, VQ_F32);
-  gate.wide = y_dtype != VQ_BF16;
+  gate.wide = ws.wide_in;
   gate.yq = ws.hq;
   gate.ys = ws.hs;
   F8Args last = product(M, D, I, w_out, s_out, nullptr, 0, y, y_dtype);
   auto run = [&](bool check_only) {
-    const vq_status st = linear(gate, x, x_dtype, ldx, in, stream, check_only);
+    const vq_status st = linear(gate, x, x_dtype, ldx, ws.in, stream, check_only);
     if (st != VQ_OK) return st;
-    if (!ws.writes_q) return linear(last, ws.h, VQ_F32, I, out, stream, check_only);
+    if (!ws.writes_q) return linear(last, ws.h, VQ_F32, I, ws.out, stream, check_only);
     F8Args a = last;
+    a.plan = ws.out.plan;
+    a.part = ws.out.part;
     a.q = ws.hq;
     a.s = ws.hs;
-    a.splits = out.splits;
-    a.part = out.part;
     return launch_f8(a, stream, check_only);
   };
   const vq_status st = run(true);

@@ -24,13 +24,13 @@ constexpr int kSines = 1024;    // pairs of all tokens of a workgroup
 // Sum over groups of `lanes` consecutive lanes, the same bits in all of them.
 template <int CTRL>
 __device__ __forceinline__ float other(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+  return __builtin_bit_cast(float, vqd::other<CTRL>(__builtin_bit_cast(uint32_t, v)));
 }
 __device__ __forceinline__ float group_sum(float v, int lanes) {
-  if (lanes > 1) v += other<0xB1>(v);   // lane ^ 1
-  if (lanes > 2) v += other<0x4E>(v);   // lane ^ 2
-  if (lanes > 4) v += other<0x141>(v);  // the other four of 8
-  if (lanes > 8) v += other<0x140>(v);  // the other eight of 16
+  if (lanes > 1) v += other<vqd::kXor1>(v);
+  if (lanes > 2) v += other<vqd::kXor2>(v);
+  if (lanes > 4) v += other<vqd::kHalf>(v);
+  if (lanes > 8) v += other<vqd::kRow>(v);
   if (lanes > 16) v += __shfl_xor(v, 16, 64);
   if (lanes > 32) v += __shfl_xor(v, 32, 64);
   return v;

@@ -257,12 +257,19 @@ struct F8QuantArgs {
 vq_status launch_f8_tokens(const F8QuantArgs& a, void* stream, bool check_only = false);
 vq_status launch_f8_weights(const F8QuantArgs& a, void* stream);
 
+// How a product is computed (vq_f8.hip): the way, how often K is cut over the CUs, and whether the tokens are cut to 8 bits
+// inside the kernel.
+struct F8Plan {
+  int32_t way, splits;
+  bool cut;
+};
 // A product with block scales (validated arguments; vq_f8.hip).
 struct F8Args {
   int32_t m, n, k;   // n outputs (with the gate: w has 2 n rows)
-  const uint8_t* q;  // [m][q8_row_bytes(k)] e4m3, or nullptr: the tokens are cut to 8 bits inside the kernel
+  F8Plan plan;
+  const uint8_t* q;  // [m][q8_row_bytes(k)] e4m3, unless plan.cut
   const float* s;    // [f8_blocks(k)][m]
-  const void* x;     // q == nullptr: [m][k]
+  const void* x;     // plan.cut: [m][k]
   vq_dtype x_dtype;
   int64_t ldx;
   const uint8_t* w;      // [n or 2 n][q8_row_bytes(k)] e4m3
@@ -274,15 +281,13 @@ struct F8Args {
   vq_dtype y_dtype;
   uint8_t* yq;  // [m][q8_row_bytes(n)]
   float* ys;    // [f8_blocks(n)][m]
-  float* part;  // [splits][m][n] fp32 partial sums (splits > 1)
-  int32_t splits;
+  float* part;  // [plan.splits][m][n] fp32 partial sums (splits > 1)
 };
-// K splits that a product of this shape uses; its workspace is splits * m * n fp32 where splits > 1.
-int32_t f8_splits(int32_t m, int32_t n, int32_t k, bool gated);
-// Whether a product of this shape cuts its tokens to 8 bits inside the kernel.
-bool f8_cuts_inside(int32_t m, int32_t n, int32_t k, bool gated);
-// Whether a gated product of this shape can write its outputs in 8 bits (yq, ys).
-bool f8_writes_q(int32_t m, int32_t n, int32_t k);
+// The plan of a product of m >= 1 rows and n >= 1 outputs; may_cut: the tokens come as they are, and a plan that does not cut
+// them inside pays for the launch that does.
+F8Plan f8_plan(int32_t m, int32_t n, int32_t k, bool gated, bool wide, bool may_cut);
+// A gated product whose outputs are to be cut to 8 bits, by `plan` as it is or, true, by one that writes them so (yq, ys).
+bool f8_big_plan(int32_t m, int32_t n, int32_t k, bool wide, F8Plan& plan);
 vq_status launch_f8(const F8Args& a, void* stream, bool check_only = false);
 
 // Norms and rotation of heads (validated arguments; vq_heads.hip).
