@@ -18,8 +18,9 @@ namespace {
 using vqi::HeadsArgs;
 
 constexpr int kThreads = 256;
-constexpr int kItem = 16;       // values per lane and item
-constexpr int kSines = 1024;    // pairs of all tokens of a workgroup
+constexpr int kSines = 1024;  // pairs of all tokens of a workgroup
+// Pairs of a token in LDS: whole pieces of 8, read as such.
+constexpr int32_t pairs_of(int32_t rot) { return (rot / 2 + 7) / 8 * 8; }
 
 // Sum over groups of `lanes` consecutive lanes, the same bits in all of them.
 template <int CTRL>
@@ -36,38 +37,46 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
-// Where a lane's item lies in a head: 8 values from `a` on and 8 from `b` on, `na` and `nb` of them there; `pair` is its
-// first pair, or -1 beside the rotated part.
+// Where a lane's item lies in a head: 8 values from `a` on and 8 from `b` on, `na` and `nb` of them there.  Neighbouring
+// lanes take neighbouring pieces of 8 of a part, and as many further on the other halves of their items, so that every load
+// and store of a wavefront is one run.  `pair`, `pair_b`: the first pairs of the two halves (half layout: of the first four
+// and the next four of the item's pairs), -1 beside the rotated part.
 struct Item {
-  int32_t a, b, na, nb, pair;
+  int32_t a, b, na, nb, pair, pair_b;
 };
 __device__ __forceinline__ Item item_at(const HeadsArgs& h, int32_t i) {
-  Item r{0, 0, 0, 0, -1};
+  Item r{0, 0, 0, 0, -1, -1};
   const int32_t half = h.rot / 2, front = (h.start + 15) / 16, turned = (half + 7) / 8;
-  int32_t at, end;
+  int32_t from, end, items;
   if (i < front) {
-    at = i * 16;
+    from = 0;
     end = h.start;
+    items = front;
   } else if (i < front + turned) {
-    r.pair = (i - front) * 8;
-    const int32_t n = min(8, half - r.pair);
-    if (h.interleaved) {
-      at = h.start + 2 * r.pair;
-      end = at + 2 * n;
-    } else {
+    i -= front;
+    if (!h.interleaved) {
+      r.pair = 8 * i;
+      r.pair_b = r.pair + 4;
       r.a = h.start + r.pair;
       r.b = r.a + half;
-      r.na = r.nb = n;
+      r.na = r.nb = min(8, half - r.pair);
       return r;
     }
+    from = h.start;
+    end = from + h.rot;
+    items = turned;
+    r.pair = 4 * i;
+    r.pair_b = 4 * (i + items);
   } else {
-    at = h.start + h.rot + (i - front - turned) * 16;
+    i -= front + turned;
+    from = h.start + h.rot;
     end = h.dim;
+    items = (end - from + 15) / 16;
   }
-  r.a = at;
-  r.b = at + 8;
-  r.na = min(max(end - at, 0), 8);
-  r.nb = min(max(end - at - 8, 0), 8);
+  r.a = from + 8 * i;
+  r.b = r.a + 8 * items;
+  r.na = i < items ? min(max(end - r.a, 0), 8) : 0;  // lanes beyond the last item hold nothing
+  r.nb = i < items ? min(max(end - r.b, 0), 8) : 0;
   return r;
 }
 inline int32_t items_of(const HeadsArgs& h) {
@@ -104,13 +113,18 @@ __device__ __forceinline__ float value(const uint32_t (&v)[Bits<XT>::kWords], in
     return vqd::x_to_f32<XT == VQ_F16 ? 0 : 1>(v[k / 2] >> (16 * (k & 1)));
   }
 }
+// `n` of 8 values of a vector at `at`; zeros behind.
 __device__ __forceinline__ void load_vec(const void* p, vq_dtype t, int32_t at, int32_t n, float* f) {
+  if (t == VQ_F32) {
+    uint32_t v[8];
+    load_bits<VQ_F32>((const char*)p + (int64_t)at * 4, n, v);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    f[k] = 0.f;
-    if (k < n)
-      f[k] = t == VQ_F32 ? ((const float*)p)[at + k]
-                         : t == VQ_F16 ? vqd::f16_to_f32(((const uint16_t*)p)[at + k]) : vqd::bf16_to_f32(((const uint16_t*)p)[at + k]);
+    for (int k = 0; k < 8; ++k) f[k] = value<VQ_F32>(v, k);
+  } else {
+    uint32_t v[4];
+    load_bits<VQ_F16>((const char*)p + (int64_t)at * 2, n, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = t == VQ_F16 ? value<VQ_F16>(v, k) : value<VQ_BF16>(v, k);
   }
 }
 __device__ __forceinline__ void store_part(char* row, vq_dtype t, int32_t at, int32_t n, const float* f) {
@@ -141,22 +155,30 @@ __device__ __forceinline__ void store_part(char* row, vq_dtype t, int32_t at, in
 }
 
 // A workgroup takes `tt` tokens (of batch * tokens, from blockIdx.x * tt on) and `per` heads (of queries and keys in a row,
-// from blockIdx.y * per on); its groups of `lanes` lanes take one head of one token after the other.  I items per lane.
-template <int I, int NORM, vq_dtype XT>
+// from blockIdx.y * per on).  Its groups of `lanes` lanes are dealt to the tokens, 256 / lanes / tt to each, and take its
+// heads in turn, with the token's sines in registers and the next head on its way.  I items per lane.
+template <int I, int NORM, vq_dtype XT, bool INTER>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a, int32_t lanes, int32_t tt, int32_t per) {
-  __shared__ float cs[kSines], sn[kSines];
+  __shared__ __attribute__((aligned(16))) float cs[kSines], sn[kSines];
   const int64_t all = (int64_t)a.batch * a.tokens;
   const int64_t bt0 = (int64_t)blockIdx.x * tt;
   const int32_t here = (int32_t)min((int64_t)tt, all - bt0);
-  const int32_t half = a.rot / 2;
-  const int32_t groups = kThreads / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int32_t half = a.rot / 2, pairs = pairs_of(a.rot);
+  const int32_t groups = kThreads / lanes / tt, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int32_t mine = group / groups, sub = group % groups;  // this group's token, and which of the token's groups it is
+  const bool there = mine < here;  // idle groups go along: barriers, and sums over whole groups of lanes
+  const int64_t bt = bt0 + (there ? mine : 0), b = bt / a.tokens, t = bt - b * a.tokens;
   constexpr int es = XT == VQ_F32 ? 4 : 2;
   const int ey = a.y_dtype == VQ_F32 ? 4 : 2;
 
+  Item it[I];
+#pragma unroll
+  for (int n = 0; n < I; ++n) it[n] = item_at(a, lane + n * lanes);
+
   for (int32_t i = threadIdx.x; i < here * half; i += kThreads) {
     const int32_t tok = i / half, j = i - tok * half;
-    const int64_t bt = bt0 + tok;
-    const int64_t b = bt / a.tokens, at = b * a.pos_stride + (bt - b * a.tokens);
+    const int64_t p_bt = bt0 + tok;
+    const int64_t p_b = p_bt / a.tokens, at = p_b * a.pos_stride + (p_bt - p_b * a.tokens);
     const double p = a.pos_64 ? (double)((const int64_t*)a.positions)[at] : (double)((const int32_t*)a.positions)[at];
     const double turn = p * a.freqs[j];
     const double r = turn - __builtin_rint(turn);
@@ -165,14 +187,19 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a, int32_t la
     sincospif((float)(2.0 * (r - 0.25 * quarter)), &s, &c);  // up to a quarter of a half turn
     const int q = (int)quarter & 3;
     const float c1 = q & 1 ? s : c, s1 = q & 1 ? c : s;
-    cs[i] = (q == 1 || q == 2 ? -c1 : c1) * a.scale;
-    sn[i] = (q >= 2 ? -s1 : s1) * a.scale;
+    cs[tok * pairs + j] = (q == 1 || q == 2 ? -c1 : c1) * a.scale;
+    sn[tok * pairs + j] = (q >= 2 ? -s1 : s1) * a.scale;
   }
   __syncthreads();
-
-  Item it[I];
+  float co[I][8], si[I][8];  // pairs past the part's end: what the array holds, for values that are not stored
 #pragma unroll
-  for (int n = 0; n < I; ++n) it[n] = item_at(a, lane + n * lanes);
+  for (int n = 0; n < I; ++n) {
+    const int32_t at = (there ? mine : 0) * pairs, p = at + max(it[n].pair, 0), q = at + max(it[n].pair_b, 0);
+    __builtin_memcpy(co[n], cs + p, 16);
+    __builtin_memcpy(co[n] + 4, cs + q, 16);
+    __builtin_memcpy(si[n], sn + p, 16);
+    __builtin_memcpy(si[n] + 4, sn + q, 16);
+  }
   const float inv_d = 1.0f / (float)a.dim;
 
   for (int part = 0; part < 2; ++part) {
@@ -180,44 +207,40 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a, int32_t la
     const int32_t h0 = max((int32_t)blockIdx.y * per - first, 0);
     const int32_t h1 = min(((int32_t)blockIdx.y + 1) * per - first, a.heads[part]);
     if (h0 >= h1) continue;
-    const int32_t count = h1 - h0, units = here * count;
-    float w[NORM ? I : 1][16], bias[NORM ? I : 1][16];
+    const char* const x = (const char*)a.x[part] + (b * a.xs[part][0] + t * a.xs[part][1]) * es;
+    char* const y = (char*)a.y[part] + (b * a.ys[part][0] + t * a.ys[part][1]) * ey;
+    Bits<XT> raw[I];
+    auto ask = [&](int32_t h) {  // a head past the last one is the first again
+      const char* p = x + (int64_t)(h < h1 ? h : h0) * a.xs[part][2] * es;
+#pragma unroll
+      for (int n = 0; n < I; ++n) {
+        load_bits<XT>(p + (int64_t)it[n].a * es, it[n].na, raw[n].v[0]);
+        load_bits<XT>(p + (int64_t)it[n].b * es, it[n].nb, raw[n].v[1]);
+      }
+    };
+    ask(h0 + sub);
+    float w[NORM ? I : 1][16];
     if constexpr (NORM) {
 #pragma unroll
       for (int n = 0; n < I; ++n) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          w[n][k] = 1.f;
-          bias[n][k] = 0.f;
-        }
+        for (int k = 0; k < 16; ++k) w[n][k] = 1.f;
         if (a.w[part]) {
           load_vec(a.w[part], a.w_dtype, it[n].a, it[n].na, w[n]);
           load_vec(a.w[part], a.w_dtype, it[n].b, it[n].nb, w[n] + 8);
 #pragma unroll
           for (int k = 0; k < 16; ++k) w[n][k] += a.w_offset;
         }
-        if (a.b[part]) {
-          load_vec(a.b[part], a.w_dtype, it[n].a, it[n].na, bias[n]);
-          load_vec(a.b[part], a.w_dtype, it[n].b, it[n].nb, bias[n] + 8);
-        }
       }
     }
-    for (int32_t u0 = 0; u0 < units; u0 += groups) {
-      const int32_t u = u0 + group;
-      const bool there = u < units;  // idle lanes go along: the sums are over whole groups of lanes
-      const int32_t tok = there ? u / count : 0, h = there ? h0 + u - tok * count : h0;
-      const int64_t bt = bt0 + tok, b = bt / a.tokens, t = bt - b * a.tokens;
-      const char* x = (const char*)a.x[part] + (b * a.xs[part][0] + t * a.xs[part][1] + h * a.xs[part][2]) * es;
-      char* y = (char*)a.y[part] + (b * a.ys[part][0] + t * a.ys[part][1] + h * a.ys[part][2]) * ey;
+    for (int32_t hp = h0; hp < h1; hp += groups) {
+      const int32_t h = hp + sub;
       float f[I][16];
 #pragma unroll
-      for (int n = 0; n < I; ++n) {
-        Bits<XT> raw;
-        load_bits<XT>(x + (int64_t)it[n].a * es, it[n].na, raw.v[0]);
-        load_bits<XT>(x + (int64_t)it[n].b * es, it[n].nb, raw.v[1]);
+      for (int n = 0; n < I; ++n)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) f[n][k] = value<XT>(raw.v[k / 8], k % 8);
-      }
+        for (int k = 0; k < 16; ++k) f[n][k] = value<XT>(raw[n].v[k / 8], k % 8);
+      if (hp + groups < h1) ask(h + groups);
       if constexpr (NORM != VQ_NORM_NONE) {
         if constexpr (NORM == VQ_NORM_LAYER) {
           float sum = 0.f;
@@ -238,42 +261,55 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a, int32_t la
           for (int k = 0; k < 16; ++k) sq = __builtin_fmaf(f[n][k], f[n][k], sq);
         const float inv = 1.0f / __builtin_sqrtf(group_sum(sq, lanes) * inv_d + a.eps);
 #pragma unroll
-        for (int n = 0; n < I; ++n)
+        for (int n = 0; n < I; ++n) {
+          if (a.b[part]) {
+            float bias[16];
+            load_vec(a.b[part], a.w_dtype, it[n].a, it[n].na, bias);
+            load_vec(a.b[part], a.w_dtype, it[n].b, it[n].nb, bias + 8);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) f[n][k] = __builtin_fmaf(f[n][k] * inv, w[n][k], bias[n][k]);
+            for (int k = 0; k < 16; ++k) f[n][k] = __builtin_fmaf(f[n][k] * inv, w[n][k], bias[k]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[n][k] = f[n][k] * inv * w[n][k];
+          }
+        }
       }
 #pragma unroll
       for (int n = 0; n < I; ++n) {
         if (it[n].pair >= 0) {
-          const int32_t at = tok * half + it[n].pair;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int32_t j = at + (it[n].pair + k < half ? k : 0);
-            const float c = cs[j], s = sn[j];
-            float& p = a.interleaved ? f[n][2 * k] : f[n][k];
-            float& q = a.interleaved ? f[n][2 * k + 1] : f[n][8 + k];
-            const float p1 = __builtin_fmaf(p, c, -(q * s)), q1 = __builtin_fmaf(p, s, q * c);
-            p = p1;
-            q = q1;
+            const float u = INTER ? f[n][2 * k] : f[n][k], v = INTER ? f[n][2 * k + 1] : f[n][8 + k];
+            (INTER ? f[n][2 * k] : f[n][k]) = __builtin_fmaf(u, co[n][k], -(v * si[n][k]));
+            (INTER ? f[n][2 * k + 1] : f[n][8 + k]) = __builtin_fmaf(u, si[n][k], v * co[n][k]);
           }
         }
-        if (there) {
-          store_part(y, a.y_dtype, it[n].a, it[n].na, f[n]);
-          store_part(y, a.y_dtype, it[n].b, it[n].nb, f[n] + 8);
+        if (there && h < h1) {
+          char* p = y + (int64_t)h * a.ys[part][2] * ey;
+          store_part(p, a.y_dtype, it[n].a, it[n].na, f[n]);
+          store_part(p, a.y_dtype, it[n].b, it[n].nb, f[n] + 8);
         }
       }
     }
   }
 }
 
+template <int I, int NORM, vq_dtype XT>
+void launch_t(const HeadsArgs& a, dim3 g, int32_t lanes, int32_t tt, int32_t per, hipStream_t st) {
+  if (a.interleaved) heads_kernel<I, NORM, XT, true><<<g, dim3(kThreads), 0, st>>>(a, lanes, tt, per);
+  else heads_kernel<I, NORM, XT, false><<<g, dim3(kThreads), 0, st>>>(a, lanes, tt, per);
+}
 template <int I, int NORM>
 void launch(const HeadsArgs& a, dim3 g, int32_t lanes, int32_t tt, int32_t per, hipStream_t st) {
   switch (a.x_dtype) {
-    case VQ_F32: heads_kernel<I, NORM, VQ_F32><<<g, dim3(kThreads), 0, st>>>(a, lanes, tt, per); break;
-    case VQ_F16: heads_kernel<I, NORM, VQ_F16><<<g, dim3(kThreads), 0, st>>>(a, lanes, tt, per); break;
-    default: heads_kernel<I, NORM, VQ_BF16><<<g, dim3(kThreads), 0, st>>>(a, lanes, tt, per);
+    case VQ_F32: launch_t<I, NORM, VQ_F32>(a, g, lanes, tt, per, st); break;
+    case VQ_F16: launch_t<I, NORM, VQ_F16>(a, g, lanes, tt, per, st); break;
+    default: launch_t<I, NORM, VQ_BF16>(a, g, lanes, tt, per, st);
   }
 }
+
+// Workgroups up to which a token's heads are spread over more lanes rather than taken in turn: two for each CU.
+constexpr int64_t kWorkgroups = 512;
 
 }  // namespace
 
@@ -287,12 +323,10 @@ vq_status launch_heads(const HeadsArgs& a, void* stream) {
   if (items > 2 * lanes) return VQ_ERR_SHAPE;
   const int64_t all = (int64_t)a.batch * a.tokens;
   const int32_t heads = a.heads[0] + a.heads[1], groups = kThreads / lanes;
-  int32_t tt = 1, per = groups;
-  if (all >= 1024) {
-    per = heads;
-    tt = 4;
-  }
-  while (tt > 1 && tt * (a.rot / 2) > kSines) tt /= 2;
+  // tokens of a workgroup: as many as leave each group of lanes 16 heads at most, fit the sines' place and leave the CUs work
+  int32_t tt = groups, per = heads;
+  while (tt > 1 && (tt * pairs_of(a.rot) > kSines || groups / tt * 16 < heads || (all + tt - 1) / tt < kWorkgroups)) tt /= 2;
+  if (tt == 1 && all < kWorkgroups) per = groups;  // one head for each group
   const int64_t gx = (all + tt - 1) / tt, gy = ((int64_t)heads + per - 1) / per;
   if (gy > 65535 || !grid_ok(gx * gy, kThreads)) return VQ_ERR_SHAPE;
   const dim3 g((uint32_t)gx, (uint32_t)gy);

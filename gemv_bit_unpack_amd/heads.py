@@ -110,27 +110,59 @@ class Rotary:
         if start < 0:
             raise ValueError("start must not be negative, got %d" % start)
         self.dim, self.start, self.interleaved = int(dim), int(start), bool(interleaved)
-        self.freqs = torch.tensor([f / (2 * math.pi) for f in freqs], dtype=torch.float64, device=device)  # turns
+        # turns per position; held here and not to be replaced: the calls take the pointer below
+        self.freqs = torch.tensor([f / (2 * math.pi) for f in freqs], dtype=torch.float64, device=device)
+        self._p, self._dev = self.freqs.data_ptr(), self.freqs.get_device()
 
 
-def _heads(t, what):
-    """(pointer, (batch, tokens, heads, dim), strides of the first three, device index) of [tokens, heads, dim] or [batch,
-    tokens, heads, dim] whose heads are contiguous."""
-    if t.dim() not in (3, 4):
-        raise ValueError("%s must be [tokens, heads, dim] or [batch, tokens, heads, dim], got %s" % (what, tuple(t.shape)))
-    shape, strides = tuple(t.shape), t.stride()
-    if shape[-1] > 1 and strides[-1] != 1:
+def _view(shape, strides, what):
+    """(batch, tokens, heads, dim) and the strides of the first three of [tokens, heads, dim] or [batch, tokens, heads, dim]
+    whose heads are contiguous; strides None: of a contiguous tensor."""
+    if len(shape) not in (3, 4):
+        raise ValueError("%s must be [tokens, heads, dim] or [batch, tokens, heads, dim], got %s" % (what, tuple(shape)))
+    *batch, n, h, d = shape
+    if strides is None:
+        strides = (n * h * d, h * d, d, 1)[4 - len(shape):]
+    if strides[-1] != 1 and d > 1:
         raise ValueError("%s must have contiguous heads" % what)
-    if t.dim() == 3:
-        shape, strides = (1,) + shape, (0,) + strides
-    return t.data_ptr(), shape, strides[:3], _device(t, what)
+    return (batch[0] if batch else 1, n, h, d), tuple(strides[:3]) if batch else (0,) + tuple(strides[:2])
 
 
 @functools.lru_cache(maxsize=1024)
-def _desc(*fields):
-    """A vq_heads_desc, by reference (it is only read); plain numbers and tuples of them only."""
+def _plan(q, k, positions, q_out, k_out, wide, rot, start, inter, kind, x_dtype, y_dtype, w_dtype, scale, eps, w_offset):
+    """A vq_heads_desc, by reference (it is only read), of tensors given by their shapes and strides, checked once for all
+    tensors alike.  Nothing here stands for a tensor itself or for its values."""
+    (b, t, hq, d), qs = _view(*q, "q")
+    hk, ks, kys = 0, (0, 0, 0), (0, 0, 0)
+    if k is not None:
+        (kb, kt, hk, kd), ks = _view(*k, "k")
+        if kt != t or kd != d or kb != b or len(k[0]) != len(q[0]):
+            raise ValueError("k must have q's batch, tokens and dim, got %s and %s" % (tuple(k[0]), tuple(q[0])))
+        kys = _view(k[0], k_out, "k_out")[1]
+    qys = _view(q[0], q_out, "q_out")[1]
+    if start + rot > d:
+        raise ValueError("the rotated part ends at %d, a head at %d" % (start + rot, d))
+    pos_stride = 0
+    if positions is not None and tuple(positions) != (t,):
+        if len(q[0]) != 4 or tuple(positions) != (b, t):
+            raise ValueError("positions must be [%d]%s, got %s" % (t, " or [%d, %d]" % (b, t) if len(q[0]) == 4 else "",
+                                                                  tuple(positions)))
+        pos_stride = t
     triple = ctypes.c_int64 * 3
-    return ctypes.byref(HeadsDesc(*[triple(*f) if isinstance(f, tuple) else f for f in fields]))
+    return ctypes.byref(HeadsDesc(b, t, hq, hk, d, rot, start, inter, kind, _code(x_dtype), _code(y_dtype),
+                                  VQ_F32 if w_dtype is None else _code(w_dtype), wide, pos_stride, triple(*qs), triple(*ks),
+                                  triple(*qys), triple(*kys), scale, eps, w_offset))
+
+
+def _output(x, out, dtype, dev, what):
+    """The output of x: (tensor, its strides or None for contiguous), a new one or `out`."""
+    if out is None:
+        return x.new_empty(x.shape, dtype=dtype), None
+    if out.shape != x.shape:
+        raise ValueError("%s must be %s, got %s" % (what, list(x.shape), tuple(out.shape)))
+    if out.get_device() != dev or out.dtype is not dtype:
+        raise ValueError("%s must be %s on device %d, is %s on %s" % (what, dtype, dev, out.dtype, out.device))
+    return out, out.stride()
 
 
 def rotate_heads(q, k, positions, rotary, *, norm="none", q_weight=None, q_bias=None, k_weight=None, k_bias=None, eps=1e-6,
@@ -147,56 +179,40 @@ def rotate_heads(q, k, positions, rotary, *, norm="none", q_weight=None, q_bias=
     kind = _KINDS.get(norm)
     if kind is None:
         raise ValueError("norm must be one of %s" % (tuple(_KINDS),))
-    qp, (b, t, hq, d), qs, dev = _heads(q, "q")
-    x_code, y_dtype = _code(q.dtype), out_dtype or (q.dtype if q_out is None else q_out.dtype)
-
-    def output(x, out, what):
-        if out is None:
-            out = torch.empty(x.shape, dtype=y_dtype, device=x.device)
-        elif out.shape != x.shape:
-            raise ValueError("%s must be %s, got %s" % (what, list(x.shape), tuple(out.shape)))
-        p, _, strides, o_dev = _heads(out, what)
-        if o_dev != dev or out.dtype is not y_dtype:
-            raise ValueError("%s must be %s on device %d, is %s on %s" % (what, y_dtype, dev, out.dtype, out.device))
-        return out, p, strides
-
-    q_out, qyp, qys = output(q, q_out, "q_out")
-    kp = kyp = None
-    hk, ks, kys = 0, (0, 0, 0), (0, 0, 0)
+    dev, x_dtype = _device(q, "q"), q.dtype
+    y_dtype = out_dtype or (x_dtype if q_out is None else q_out.dtype)
+    q_out, q_strides = _output(q, q_out, y_dtype, dev, "q_out")
+    k_view = k_strides = kp = kyp = None
     if k is not None:
-        kp, shape, ks, k_dev = _heads(k, "k")
-        if k.dim() != q.dim() or shape[:2] != (b, t) or shape[3] != d or k_dev != dev or k.dtype is not q.dtype:
-            raise ValueError("k must have q's batch, tokens, dim, dtype and device, got %s %s on %s"
-                             % (tuple(k.shape), k.dtype, k.device))
-        hk = shape[2]
-        k_out, kyp, kys = output(k, k_out, "k_out")
+        if k.dtype is not x_dtype or k.get_device() != dev:
+            raise ValueError("k must have q's dtype and device, got %s on %s" % (k.dtype, k.device))
+        k_out, k_strides = _output(k, k_out, y_dtype, dev, "k_out")
+        k_view, kp, kyp = (k.shape, k.stride()), k.data_ptr(), k_out.data_ptr()
     elif k_out is not None or k_weight is not None or k_bias is not None:
         raise ValueError("k_out, k_weight and k_bias go with k")
-    w_dtype, vecs = None, []
-    for v in (q_weight, q_bias, k_weight, k_bias):
-        if v is not None:
-            w_dtype = w_dtype or v.dtype
-            if v.dtype is not w_dtype:
-                raise TypeError("norm weights and biases must share one dtype")
-        vecs.append(_ptr(v, "a norm weight or bias", (d,), dev))
-    pos_p, wide, pos_stride, freqs_p = None, 0, 0, None
-    rot = start = inter = 0
+    w_dtype, vecs = None, (None, None, None, None)
+    if q_weight is not None or q_bias is not None or k_weight is not None or k_bias is not None:
+        vecs, dim = [q_weight, q_bias, k_weight, k_bias], (q.shape[-1],)
+        for i, v in enumerate(vecs):
+            if v is not None:
+                if w_dtype is None:
+                    w_dtype = v.dtype
+                elif v.dtype is not w_dtype:
+                    raise TypeError("norm weights and biases must share one dtype")
+                vecs[i] = _ptr(v, "a norm weight or bias", dim, dev)
+    pos = pos_p = freqs_p = None
+    wide = rot = start = inter = 0
     scale = 1.0
     if rotary is not None:
-        rot, start, inter, scale = rotary.dim, rotary.start, int(rotary.interleaved), rotary.scale
-        if start + rot > d:
-            raise ValueError("the rotated part ends at %d, a head at %d" % (start + rot, d))
-        freqs_p = _ptr(rotary.freqs, "rotary's frequencies", (rot // 2,), dev, torch.float64)
-        if positions.dtype not in (torch.int32, torch.int64):
+        rot, start, inter, scale, freqs_p = rotary.dim, rotary.start, int(rotary.interleaved), rotary.scale, rotary._p
+        if rotary._dev != dev:
+            raise ValueError("rotary must be on device %d, is on %s" % (dev, rotary.freqs.device))
+        if positions.dtype is torch.int64:
+            wide = 1
+        elif positions.dtype is not torch.int32:
             raise TypeError("positions has dtype %s, expected int32 or int64" % positions.dtype)
-        wide = int(positions.dtype is torch.int64)
-        if tuple(positions.shape) not in ((t,), (b, t)) or (positions.dim() == 2 and q.dim() == 3):
-            raise ValueError("positions must be [%d]%s, got %s" % (t, " or [%d, %d]" % (b, t) if q.dim() == 4 else "",
-                                                                  tuple(positions.shape)))
-        pos_p = _ptr(positions, "positions", None, dev)
-        pos_stride = t if positions.dim() == 2 else 0
-    desc = _desc(b, t, hq, hk, d, rot, start, inter, kind, x_code, _code(y_dtype), VQ_F32 if w_dtype is None else _code(w_dtype),
-                 wide, pos_stride, tuple(qs), tuple(ks), tuple(qys), tuple(kys), float(scale) + 0.0, float(eps) + 0.0,
-                 float(weight_offset) + 0.0)
-    _launch(lib().vq_rotate_heads, dev, desc, qp, kp, pos_p, freqs_p, *vecs, qyp, kyp, _stream(dev))
+        pos, pos_p = positions.shape, _ptr(positions, "positions", None, dev)
+    desc = _plan((q.shape, q.stride()), k_view, pos, q_strides, k_strides, wide, rot, start, inter, kind, x_dtype, y_dtype,
+                 w_dtype, float(scale) + 0.0, float(eps) + 0.0, float(weight_offset) + 0.0)  # + 0.0: -0.0 is found as 0.0
+    _launch(lib().vq_rotate_heads, dev, desc, q.data_ptr(), kp, pos_p, freqs_p, *vecs, q_out.data_ptr(), kyp, _stream(dev))
     return q_out, k_out

@@ -164,6 +164,7 @@ def test_refusals(vq):
     pos = torch.zeros(3, dtype=torch.int64, device="cuda")
     r = vq.Rotary(8)
     for call in (lambda: vq.rotate_heads(x.transpose(2, 3), None, pos, r),             # heads not contiguous
+                 lambda: vq.rotate_heads(x[0, 0], None, pos, r), lambda: vq.rotate_heads(x, x[0], pos, r),
                  lambda: vq.rotate_heads(x, x[:, :2], pos, r),                          # other tokens
                  lambda: vq.rotate_heads(x, x.half(), pos, r),                          # other type
                  lambda: vq.rotate_heads(x, None, pos[:2], r),                          # other positions
