@@ -902,30 +902,31 @@ struct Cost {
   float start, round, step[3];
 };
 constexpr Cost kCosts[2][kWays] = {
-    {{16, 4, 16, 4, 8, 2, 2.20f, 0.f, {0.85f, 1.74f}},
-     {16, 4, 32, 5, 8, 2, 1.83f, 0.f, {1.38f, 2.62f}},
-     {32, 5, 32, 5, 2, 2, 1.42f, 1.58f, {0.32f, 0.51f}},
-     {32, 5, 64, 6, 1, 3, 1.75f, 1.74f, {0.27f, 0.41f, 0.51f}},
-     {64, 6, 64, 6, 2, 1, 0.66f, 2.63f, {0.54f}},
-     {64, 6, 128, 7, 1, 2, 1.33f, 2.49f, {0.45f, 0.84f}},
-     {128, 7, 128, 7, 1, 1, 2.20f, 3.48f, {0.62f}},
-     {128, 7, 128, 7, 1, 2, 2.04f, 4.04f, {0.72f, 1.09f}},
+    {{16, 4, 16, 4, 8, 2, 1.76f, 0.f, {0.82f, 1.79f}},
+     {16, 4, 32, 5, 8, 2, 1.64f, 0.f, {1.33f, 2.61f}},
+     {32, 5, 32, 5, 2, 2, 1.46f, 1.54f, {0.32f, 0.53f}},
+     {32, 5, 64, 6, 1, 3, 1.13f, 1.94f, {0.26f, 0.43f, 0.52f}},
+     {64, 6, 64, 6, 2, 1, 0.64f, 2.63f, {0.55f}},
+     {64, 6, 128, 7, 1, 2, 0.91f, 2.52f, {0.44f, 0.85f}},
+     {128, 7, 128, 7, 1, 1, 1.51f, 3.64f, {0.61f}},
+     {128, 7, 128, 7, 1, 2, 1.24f, 4.19f, {0.71f, 1.11f}},
      {256, 8, 256, 8, 1, 1, 2.87f, 8.20f, {1.73f}}},
     // operands in fp16
-    {{16, 4, 16, 4, 8, 2, 2.20f, 0.f, {0.85f, 1.74f}},
-     {16, 4, 32, 5, 8, 2, 1.83f, 0.f, {1.38f, 2.62f}},
-     {32, 5, 32, 5, 2, 2, 1.28f, 1.72f, {0.40f, 0.64f}},
-     {32, 5, 64, 6, 1, 3, 0.66f, 2.68f, {0.36f, 0.62f, 0.65f}},
-     {64, 6, 64, 6, 2, 1, 0.66f, 2.67f, {0.77f}},
-     {64, 6, 128, 7, 1, 2, 0.00f, 3.64f, {0.71f, 1.52f}},
-     {128, 7, 128, 7, 1, 1, 1.31f, 3.83f, {1.08f}},
-     {128, 7, 128, 7, 1, 2, 1.73f, 4.57f, {1.13f, 1.88f}},
+    {{16, 4, 16, 4, 8, 2, 1.76f, 0.f, {0.82f, 1.79f}},
+     {16, 4, 32, 5, 8, 2, 1.64f, 0.f, {1.33f, 2.61f}},
+     {32, 5, 32, 5, 2, 2, 1.30f, 1.70f, {0.40f, 0.65f}},
+     {32, 5, 64, 6, 1, 3, 0.14f, 2.85f, {0.35f, 0.62f, 0.66f}},
+     {64, 6, 64, 6, 2, 1, 0.66f, 2.66f, {0.78f}},
+     {64, 6, 128, 7, 1, 2, 0.00f, 3.34f, {0.69f, 1.54f}},
+     {128, 7, 128, 7, 1, 1, 0.87f, 3.95f, {1.06f}},
+     {128, 7, 128, 7, 1, 2, 1.27f, 4.65f, {1.11f, 1.89f}},
      {128, 7, 256, 8, 1, 1, 0.92f, 5.69f, {1.75f}}}};  // only where it writes its outputs in 8 bits
 // Cutting tokens to 8 bits: inside the streaming kernel (its start, and for each 64 pieces of 16 columns of a wavefront),
 // and in a launch of its own (and its bytes per us).
-constexpr float kCutStart[2] = {1.3f, 1.4f}, kCutPiece = 0.9f, kQuantStart = 3.3f, kQuantRate = 4e6f;
+constexpr float kCutStart[2] = {1.45f, 1.44f}, kCutPiece = 0.9f, kQuantStart = 3.3f, kQuantRate = 4e6f;
 constexpr float kCopyRate = 5.3e6f, kCopyStart = 2.0f;   // bytes per us of a large copy
-constexpr float kJoinStart = 2.6f, kJoinRate = 4.5e6f;   // the launch that adds up a cut K
+constexpr float kJoinStart = 3.6f, kJoinRate = 4.5e6f;   // the launch that adds up a cut K,
+constexpr float kJoinMargin = 1.06f;                     // which has to win by so much
 
 int32_t ceil_div(int32_t a, int32_t b) { return (int32_t)(((uint32_t)a + (uint32_t)b - 1) / (uint32_t)b); }
 
@@ -967,8 +968,7 @@ float cost(const Shape& s, int32_t way, int32_t splits, bool cut, bool wide) {
     }
   }
   t = std::max(t, s.copy);
-  if (splits > 1) t += kJoinStart + ((float)splits * s.parts + s.out) / kJoinRate;
-  return t;
+  return splits == 1 ? t : (t + kJoinStart + ((float)splits * s.parts + s.out) / kJoinRate) * kJoinMargin;
 }
 
 vq_status stream(const F8Args& a, hipStream_t st, bool check_only) {

@@ -127,6 +127,17 @@ __device__ __forceinline__ void load_vec(const void* p, vq_dtype t, int32_t at, 
     for (int k = 0; k < 8; ++k) f[k] = t == VQ_F16 ? value<VQ_F16>(v, k) : value<VQ_BF16>(v, k);
   }
 }
+// 16 bytes, past the caches where STREAM.
+template <bool STREAM>
+__device__ __forceinline__ void store16(void* p, const uint32_t* v) {
+  if constexpr (STREAM) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+    __builtin_nontemporal_store(u4{v[0], v[1], v[2], v[3]}, (u4*)p);
+  } else {
+    __builtin_memcpy(p, v, 16);
+  }
+}
+template <bool STREAM>
 __device__ __forceinline__ void store_part(char* row, vq_dtype t, int32_t at, int32_t n, const float* f) {
   float v[8];
 #pragma unroll
@@ -134,7 +145,8 @@ __device__ __forceinline__ void store_part(char* row, vq_dtype t, int32_t at, in
   if (t == VQ_F32) {
     float* p = (float*)row + at;
     if (n == 8) {
-      __builtin_memcpy(p, v, 32);
+      store16<STREAM>(p, (const uint32_t*)v);
+      store16<STREAM>(p + 4, (const uint32_t*)v + 4);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -145,7 +157,9 @@ __device__ __forceinline__ void store_part(char* row, vq_dtype t, int32_t at, in
     vqd::narrow<8>(v, t, h);
     uint16_t* p = (uint16_t*)row + at;
     if (n == 8) {
-      __builtin_memcpy(p, h, 16);
+      uint32_t w[4];
+      __builtin_memcpy(w, h, 16);
+      store16<STREAM>(p, w);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -286,8 +300,13 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a, int32_t la
         }
         if (there && h < h1) {
           char* p = y + (int64_t)h * a.ys[part][2] * ey;
-          store_part(p, a.y_dtype, it[n].a, it[n].na, f[n]);
-          store_part(p, a.y_dtype, it[n].b, it[n].nb, f[n] + 8);
+          if (a.streams) {
+            store_part<true>(p, a.y_dtype, it[n].a, it[n].na, f[n]);
+            store_part<true>(p, a.y_dtype, it[n].b, it[n].nb, f[n] + 8);
+          } else {
+            store_part<false>(p, a.y_dtype, it[n].a, it[n].na, f[n]);
+            store_part<false>(p, a.y_dtype, it[n].b, it[n].nb, f[n] + 8);
+          }
         }
       }
     }
@@ -315,7 +334,8 @@ constexpr int64_t kWorkgroups = 512;
 
 namespace vqi {
 
-vq_status launch_heads(const HeadsArgs& a, void* stream) {
+vq_status launch_heads(const HeadsArgs& args, void* stream) {
+  HeadsArgs a = args;
   hipStream_t st = (hipStream_t)stream;
   const int32_t items = items_of(a);
   int32_t lanes = 1;
@@ -323,12 +343,19 @@ vq_status launch_heads(const HeadsArgs& a, void* stream) {
   if (items > 2 * lanes) return VQ_ERR_SHAPE;
   const int64_t all = (int64_t)a.batch * a.tokens;
   const int32_t heads = a.heads[0] + a.heads[1], groups = kThreads / lanes;
-  // tokens of a workgroup: as many as leave each group of lanes 16 heads at most, fit the sines' place and leave the CUs work
+  // tokens of a workgroup: as many as leave each group of lanes so many heads at most, fit the sines' place and leave the CUs
+  // work.  8192 tokens, 64 + 8 heads of 128, 4, 8 and 16 heads a group: rotated 59, 59 and 63 us (half a head 64, 69 and 74),
+  // with norms, whose weights a group loads once, 77, 66 and 66
+  const int32_t turns = a.norm == VQ_NORM_NONE ? 4 : 8;
   int32_t tt = groups, per = heads;
-  while (tt > 1 && (tt * pairs_of(a.rot) > kSines || groups / tt * 16 < heads || (all + tt - 1) / tt < kWorkgroups)) tt /= 2;
+  while (tt > 1 && (tt * pairs_of(a.rot) > kSines || groups / tt * turns < heads || (all + tt - 1) / tt < kWorkgroups)) tt /= 2;
   if (tt == 1 && all < kWorkgroups) per = groups;  // one head for each group
   const int64_t gx = (all + tt - 1) / tt, gy = ((int64_t)heads + per - 1) / per;
   if (gy > 65535 || !grid_ok(gx * gy, kThreads)) return VQ_ERR_SHAPE;
+  // Outputs that the L2s (8 of 4 MB) would not hold for whoever reads them next go past them: 8192 tokens of 64 + 8 heads of
+  // 128 in bf16, 151 MB each way, 74 us through the caches and 62 past them (with norms 75 and 67, half a head rotated 97 and
+  // 73); 512 tokens of 32 + 8 heads 6.7 us either way
+  a.streams = all * heads * a.dim * (a.y_dtype == VQ_F32 ? 4 : 2) > (int64_t)32 << 20;
   const dim3 g((uint32_t)gx, (uint32_t)gy);
   const bool two = items > lanes;
   switch (a.norm) {

@@ -304,6 +304,7 @@ struct HeadsArgs {
   float scale;          // on the rotated values
   const void *w[2], *b[2];  // [dim] or nullptr
   float eps, w_offset;
+  int32_t streams;  // set by launch_heads: outputs go past the caches
 };
 vq_status launch_heads(const HeadsArgs& a, void* stream);
 

@@ -104,7 +104,8 @@ def test_quantize_views(vq):
 SHAPES = [(1, 1, 1), (1, 16, 128), (1, 17, 129), (1, 128, 1000), (1, 5003, 4099), (1, 20000, 300), (1, 130, 20000), (2, 64, 64),
           (3, 777, 1030), (4, 4096, 4096), (5, 200, 4096), (16, 16, 8192), (16, 7001, 700), (17, 64, 128), (17, 65, 9000),
           (37, 5003, 4099), (64, 257, 1100), (65, 128, 128), (77, 2056, 5001), (128, 1024, 8192), (129, 129, 129), (200, 3000, 777),
-          (256, 256, 256), (300, 6500, 1000), (513, 2050, 385), (2049, 6500, 260)]
+          (256, 256, 256), (300, 6500, 1000), (513, 2050, 385), (2049, 6500, 260), (513, 7225, 130), (200, 8229, 385), (200, 8212, 1000), (130, 5485, 1000),
+          (200, 8198, 130), (1, 83, 9000), (33, 8212, 130), (3, 28672, 256), (385, 900, 9000), (130, 903, 20000), (385, 65, 20000)]
 
 
 def _exact_ints(vq, g, m, n, k, halves=1):
