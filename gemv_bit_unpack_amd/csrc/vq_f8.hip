@@ -926,7 +926,7 @@ constexpr Cost kCosts[2][kWays] = {
 constexpr float kCutStart[2] = {1.45f, 1.44f}, kCutPiece = 0.9f, kQuantStart = 3.3f, kQuantRate = 4e6f;
 constexpr float kCopyRate = 5.3e6f, kCopyStart = 2.0f;   // bytes per us of a large copy
 constexpr float kJoinStart = 3.6f, kJoinRate = 4.5e6f;   // the launch that adds up a cut K,
-constexpr float kJoinMargin = 1.06f;                     // which has to win by so much
+constexpr float kJoinMargin = 1.12f;                     // which has to win by so much
 
 int32_t ceil_div(int32_t a, int32_t b) { return (int32_t)(((uint32_t)a + (uint32_t)b - 1) / (uint32_t)b); }
 
@@ -950,7 +950,10 @@ float cost(const Shape& s, int32_t way, int32_t splits, bool cut, bool wide) {
   if (way <= kStream2) {
     // two workgroups on each CU, that take turns with the memory: parts of a round count as such
     const float rounds = (float)columns * (float)splits * (1.f / kFewWorkgroups);
-    t += steps * (rounds <= 0.5f ? c.step[0] : c.step[1] * std::max(rounds, 1.f));
+    // cut inside, single blocks with eight steps of a wavefront or more, whole sets, keep their loads going: 1 x 28672 x 8192
+    // 43 us, 48 in groups of two; 2 x 28672 x 5120 (five steps) 36 and 34
+    const float going = cut && way == kStream1 && steps >= 8.f ? 0.8f : 1.f;
+    t += steps * (rounds <= 0.5f ? c.step[0] : going * c.step[1] * std::max(rounds, 1.f));
     if (cut) t += kCutStart[way] + kCutPiece * 0.125f * (float)s.m * steps;
   } else {
     const int32_t rows = (int32_t)(((int64_t)s.m + c.bm - 1) >> c.bm_log2);
@@ -967,7 +970,8 @@ float cost(const Shape& s, int32_t way, int32_t splits, bool cut, bool wide) {
       if (rest) t += steps * c.step[rest - 1];
     }
   }
-  t = std::max(t, s.copy);
+  // streamed weights come with their tokens, from the caches: 8 and 16 rows of 28672 x 8192 53 and 60 us, 46 in tiles
+  t = std::max(t, way <= kStream2 ? s.copy * (1.f + (float)s.m * (1.f / 64)) : s.copy);
   return splits == 1 ? t : (t + kJoinStart + ((float)splits * s.parts + s.out) / kJoinRate) * kJoinMargin;
 }
 
