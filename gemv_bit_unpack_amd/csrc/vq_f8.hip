@@ -6,6 +6,9 @@
 // added to the output's fp32 sum with the product of its two scales: one fused multiply-add per output and block, beside
 // 128 multiply-adds of the matrix pipe.  That is half of the vector pipe's time under the matrix pipe's whole.
 //
+// Up to some hundred rows the weights' bytes bound it (one row of 28672 x 8192: 42 us, 5.6 TB/s), above that the matrix pipe
+// at the clock that the card holds (8192^3: 479 us, 2.3 PFLOP/s; a library product with one scale for all 414 us).
+//
 // Rows of q and w are whole 128-byte steps with zero pads, so no kernel has a K edge; rows past an edge of a tile read the
 // last valid row again and are not stored.  A sum's order is fixed by the shape (waves, then K splits, in order): equal
 // calls give equal bits, calls of different shapes may differ in the last ones.
@@ -88,7 +91,7 @@ __device__ __forceinline__ v4f multiply(const Frag<WIDE>& w, const Frag<WIDE>& t
 // ---------------------------------------------------------------- to 8 bits
 
 // Tokens: 16 lanes take a block of 128 columns, 8 each; a workgroup 16 rows by 4 blocks, all of its loads on their way
-// before the first is used.
+// before the first is used.  Bound by the bytes (4096 x 4096 in bf16: 12 us, 4.2 TB/s); few rows by the launch (4 us).
 constexpr int kQuantCols = 4;
 template <vq_dtype XT>
 __global__ __launch_bounds__(256) void f8_tokens_kernel(F8QuantArgs a) {
@@ -187,7 +190,9 @@ __device__ __forceinline__ void tile(const F8Args& a, int32_t row0, int32_t n0, 
   static_assert(SG <= kWaves, "each wavefront loads one group of scales");
   static_assert(!GATED || NI % 2 == 0, "gate and up blocks in one wavefront");
   static_assert(!OUTQ || (GATED && BN == 256 && WN * NO * 16 == 128), "a block of outputs per tile");
-  // small tiles read the next step's fragments while they multiply this one's
+  // small tiles read the next step's fragments while they multiply this one's; larger ones have registers for its weights
+  // and first token block only, asked for behind this step's last products (4096 x 14336 x 4096 270 -> 232 us, with the loads
+  // to LDS no longer waited for)
   constexpr bool AHEAD = MI + NI <= 6;
   static_assert(KG == 1 || (KG == 2 && AHEAD && !SPLIT && !OUTQ && MI * NI * 1024 * kWaves <= NB * kBuf), "sums of two groups");
 
@@ -586,6 +591,10 @@ __global__ __launch_bounds__(256) void f8_join_kernel(F8Args a) {
 // the other, and 16 tokens at most; its wavefronts cut K, their sums meet in LDS.  Two sets of U steps are in registers, one
 // on its way while the other is used, across the groups: the first steps of the next group are asked for before the sums
 // of this one meet.  The steps of a last, partial set are the last one again and left out.
+// Bound by the weights' bytes: 1 x 28672 x 8192 42 us, 5.6 TB/s.  A load takes 32 bytes of a lane's row in two pieces next
+// to each other, so that both of a memory line's halves are asked for together, and without the hint that they are read
+// once: with pieces 64 bytes apart and the hint 2 x 28672 x 5120 took 44 us, so 34.  Small products are bound by their chain
+// of latencies: 1 x 4096 x 4096 7 us, 1 x 1024 x 1024 5.
 // XT >= 0: the tokens come as they are and each wavefront cuts its own part of K to 8 bits, in LDS, once, while its first
 // weights are on their way: a block's scale needs no other wavefront, so there is no barrier and no launch in front.
 // SPLIT: workgroups cut K too (blockIdx.y), and their sums go to `part`.
@@ -682,8 +691,10 @@ __global__ __launch_bounds__(512, 4) void f8_few_kernel(F8Args a, int32_t groups
   }
   __builtin_amdgcn_sched_barrier(0);
 
-  uint8_t* const xq = lds + 8 * RT * 1024 + (int64_t)(k0 - first) * a.m * (kStep + 4);  // [steps][m][128], [steps][m] scales
-  float* const xs = (float*)(xq + (int64_t)(k1 - k0) * a.m * kStep);
+  // the workgroup's tokens [steps][m][128] and behind them their scales [steps][m]; each wavefront writes and reads its own
+  uint8_t* const tokens = lds + 8 * RT * 1024;
+  uint8_t* const xq = tokens + (int64_t)(k0 - first) * a.m * kStep;
+  float* const xs = (float*)(tokens + (int64_t)(last - first) * a.m * kStep) + (int64_t)(k0 - first) * a.m;
   if constexpr (CUT) {
     for (int32_t e0 = 0; e0 < all; e0 += 64 * kAhead) {
       if (e0 > 0) {
@@ -883,19 +894,19 @@ vq_status launch_big(const F8Args& a, hipStream_t st, bool check_only) {
 
 // A way of computing a product and what it takes, in us: `start` for the launch and its ends, and for each round over the
 // CUs `round` and then `step` for each step of K, the first of them with one workgroup on a CU, then two and three, as many
-// as `together` (the LDS) says.  Fitted to 670 shapes from 1 to 4096 rows by 64 to 28672 columns and outputs, with weights
-// from memory, where they meet what was measured to 11 - 16 % (rms); the way with the least of these times, of a copy of the
-// operands and of the join of a cut K is taken.  Over those shapes that is 1.8 % slower than the best way of each (geometric
-// mean; at the worst 33 %, 15 and 20 us).  us, in the way that is taken and in the next ones:
-//   16-bit outputs: 37 x 5003 x 4099 11.4 in 32 x 32, 13.4 in 64 x 64, 14.6 in 64 x 128 / 4; 256 x 4096 x 4096 13.5 in
-//     64 x 64, 16.3 in 32 x 64, 19.6 in 128 x 64; 512 x 4096 x 4096 18.9 in 64 x 128, 24.4 in 128 x 128, 24.6 in 64 x 64;
-//     128 x 28672 x 8192 57.5 in 128 x 128, 64.8 in pairs of them, 68.3 in 64 x 128; 128 x 8192 x 28672 63 in 128 x 128 / 4,
-//     70.3 / 3, 72 in 64 x 128 / 2; 512 x 14336 x 4096 41.3 in pairs of 128 x 128, 49 in 256 x 256, 55.7 in 64 x 128;
-//     4096 x 14336 x 4096 232 in 256 x 256, 268 in pairs of 128 x 128
-//   fp32: 512 x 4096 x 4096 27.7 in 64 x 128, 32 in 64 x 64, 41 in 128 x 128; 4096 x 14336 x 4096 457 in pairs of 128 x 128,
-//     528 in 64 x 128 with four wavefronts
-//   few rows, streamed and in tiles, tokens in 8 bits: 16 x 4096 x 4096 7.1 and 9.3; 8 x 28672 x 8192 53 and 46.7; cut
-//     inside: 4 x 4096 x 4096 8.4, 3.3 + 6.3 otherwise; 8 x 4096 x 4096 10.2, 3.3 + 6.4
+// as `together` (the LDS) says.  Fitted to 670 shapes of 1 to 4096 rows by 64 to 28672 columns and outputs, weights from
+// memory, which they meet to 10 - 17 % (rms).  The way with the least of these times, or of reading the operands, is taken:
+// over those shapes 1.8 % slower than the best of each (geometric mean), at the worst a third, of 15 us.  us, in the way that
+// is taken and in others:
+//   16-bit outputs: 37 x 5003 x 4099 11.4 in 32 x 32, 12.4 in 32 x 64, 13.4 in 64 x 64, 14.6 in 64 x 128 / 4;
+//     256 x 4096 x 4096 13.5 in 64 x 64, 16.3 in 32 x 64; 512 x 4096 x 4096 18.9 in 64 x 128, 24.4 in 128 x 128, 24.6 in
+//     64 x 64; 128 x 28672 x 8192 57.5 in 128 x 128, 64.8 in pairs of them, 68.3 in 64 x 128; 128 x 8192 x 28672 63 in
+//     128 x 128 / 4, 70.3 / 3, 72 in 64 x 128 / 2; 512 x 14336 x 4096 41.3 in pairs of 128 x 128, 49 in 256 x 256, 55.7 in
+//     64 x 128; 4096 x 14336 x 4096 232 in 256 x 256, 268 in pairs of 128 x 128
+//   fp32 outputs: 512 x 4096 x 4096 27.7 in 64 x 128, 32 in 64 x 64, 41 in 128 x 128; 4096 x 14336 x 4096 457 in pairs of
+//     128 x 128, 543 in 128 x 128
+//   few rows, streamed and in tiles, tokens in 8 bits: 16 x 4096 x 4096 7.1 and 9.3, 8 x 28672 x 8192 53 and 46.7; cut
+//     inside or by a launch in front: 1 x 4096 x 4096 7.4 and 3.3 + 6.3, 8 x 4096 x 4096 10.2 and 3.3 + 6.4
 enum Way : int32_t { kStream1, kStream2, k32x32, k32x64, k64x64, k64x128, k128x128, k128x128Pair, k256x256, kWays };
 struct Cost {
   int32_t bm, bm_log2, bn, bn_log2, groups_of_k, together;
@@ -925,8 +936,7 @@ constexpr Cost kCosts[2][kWays] = {
 // and in a launch of its own (and its bytes per us).
 constexpr float kCutStart[2] = {1.45f, 1.44f}, kCutPiece = 0.9f, kQuantStart = 3.3f, kQuantRate = 4e6f;
 constexpr float kCopyRate = 5.3e6f, kCopyStart = 2.0f;   // bytes per us of a large copy
-constexpr float kJoinStart = 3.6f, kJoinRate = 4.5e6f;   // the launch that adds up a cut K,
-constexpr float kJoinMargin = 1.12f;                     // which has to win by so much
+constexpr float kJoinStart = 4.6f, kJoinRate = 4.5e6f;   // the launch that adds up a cut K (3.6 us, and one to win by)
 
 int32_t ceil_div(int32_t a, int32_t b) { return (int32_t)(((uint32_t)a + (uint32_t)b - 1) / (uint32_t)b); }
 
@@ -972,7 +982,7 @@ float cost(const Shape& s, int32_t way, int32_t splits, bool cut, bool wide) {
   }
   // streamed weights come with their tokens, from the caches: 8 and 16 rows of 28672 x 8192 53 and 60 us, 46 in tiles
   t = std::max(t, way <= kStream2 ? s.copy * (1.f + (float)s.m * (1.f / 64)) : s.copy);
-  return splits == 1 ? t : (t + kJoinStart + ((float)splits * s.parts + s.out) / kJoinRate) * kJoinMargin;
+  return splits == 1 ? t : t + kJoinStart + ((float)splits * s.parts + s.out) / kJoinRate;
 }
 
 vq_status stream(const F8Args& a, hipStream_t st, bool check_only) {

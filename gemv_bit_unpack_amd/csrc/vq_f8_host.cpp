@@ -10,8 +10,11 @@ namespace {
 
 bool valid_k(int32_t k) { return k >= 1 && k <= kF8MaxK; }
 
+// Most rows and outputs: the edge of the last tile is still an int32.
+constexpr int32_t kMaxRows = INT32_MAX - 1024;
+
 vq_status check_sizes(int32_t M, int32_t N, int32_t K, int32_t gated) {
-  if (M < 0 || N < 0 || N > (gated ? INT32_MAX / 2 : INT32_MAX) || !valid_k(K)) return VQ_ERR_SHAPE;
+  if (M < 0 || M > kMaxRows || N < 0 || N > (gated ? INT32_MAX / 2 : kMaxRows) || !valid_k(K)) return VQ_ERR_SHAPE;
   return gated == 0 || gated == 1 ? VQ_OK : VQ_ERR_UNSUPPORTED;
 }
 
@@ -147,7 +150,7 @@ extern "C" {
 
 vq_status vq_f8_quantize(int32_t rows, int32_t k, int32_t block_rows, const void* x, vq_dtype x_dtype, int64_t ldx, void* q,
                          float* s, void* stream) {
-  if (rows < 0 || !valid_k(k) || ldx < k) return VQ_ERR_SHAPE;
+  if (rows < 0 || rows > kMaxRows || !valid_k(k) || ldx < k) return VQ_ERR_SHAPE;
   if (!valid_dtype(x_dtype) || (block_rows != 1 && block_rows != kF8Block)) return VQ_ERR_UNSUPPORTED;
   if (rows == 0) return VQ_OK;
   if (!x || !q || !s) return VQ_ERR_NULL;
@@ -227,7 +230,7 @@ vq_status vq_f8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype 
 
 vq_status vq_f8_mlp_workspace_bytes(int32_t M, int32_t D, int32_t I, size_t* nbytes) {
   if (!nbytes) return VQ_ERR_NULL;
-  if (M < 0 || !valid_k(D) || !valid_k(I)) return VQ_ERR_SHAPE;
+  if (M < 0 || M > kMaxRows || !valid_k(D) || !valid_k(I)) return VQ_ERR_SHAPE;
   *nbytes = 0;
   for (const vq_dtype t : {VQ_F16, VQ_BF16, VQ_F32}) *nbytes = std::max(*nbytes, mlp_ws(M, D, I, t, nullptr).bytes);
   return VQ_OK;
@@ -236,7 +239,7 @@ vq_status vq_f8_mlp_workspace_bytes(int32_t M, int32_t D, int32_t I, size_t* nby
 vq_status vq_f8_mlp(int32_t M, int32_t D, int32_t I, const void* x, vq_dtype x_dtype, int64_t ldx, const void* w_in,
                     const float* s_in, const void* w_out, const float* s_out, void* y, vq_dtype y_dtype, void* workspace,
                     size_t workspace_bytes, void* stream) {
-  if (M < 0 || !valid_k(D) || !valid_k(I) || ldx < D) return VQ_ERR_SHAPE;
+  if (M < 0 || M > kMaxRows || !valid_k(D) || !valid_k(I) || ldx < D) return VQ_ERR_SHAPE;
   if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype)) return VQ_ERR_UNSUPPORTED;
   if (M == 0) return VQ_OK;
   if (!x || !w_in || !s_in || !w_out || !s_out || !y || !workspace) return VQ_ERR_NULL;

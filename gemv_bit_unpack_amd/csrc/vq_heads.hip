@@ -7,8 +7,12 @@
 // of 2^-27 turns at any position.  The sines of a workgroup's tokens are computed once, one pair per thread, and shared by
 // all heads in LDS.
 //
-// A head is held by L lanes (a power of two), 16 values each: 8 pairs of the rotated part, or 16 consecutive values of the
-// parts beside it.  Every value is read once and written once; the norm's sums go over the L lanes without LDS.
+// A head is held by L lanes (a power of two), 16 values each: 8 pairs of the rotated part, or 16 values of the parts beside
+// it.  Every value is read once and written once; the norm's sums go over the L lanes, up to 16 of them without LDS.
+//
+// Bound by the bytes: 8192 tokens, 64 + 8 heads of 128 in bf16, 302 MB, 58 us rotated (5.2 TB/s; a large copy reaches 5.1)
+// and 65 us with norms, whose chain of sums the wavefronts of a CU do not quite hide.  A decode step is the launch and one
+// chain position - sine - store: 3.5 to 4 us.
 #include "vq_device.h"
 #include "vq_f8_device.h"
 #include "vq_q8_device.h"

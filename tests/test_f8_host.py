@@ -88,7 +88,8 @@ def test_product_refusals(vq):
     def call(m=64, n=64, k=64, q=P, s=P, w=P, sw=P, b=None, g=0, y=P, dt=F16, ws=None, nb=0):
         return f(m, n, k, q, s, w, sw, b, g, y, dt, ws, nb, None)
 
-    for kw in (dict(m=-1), dict(n=-1), dict(k=0), dict(k=65537), dict(n=1 << 30, g=1), dict(m=2 ** 31 - 1, n=2 ** 31 - 1)):
+    for kw in (dict(m=-1), dict(n=-1), dict(k=0), dict(k=65537), dict(n=1 << 30, g=1), dict(m=2 ** 31 - 1, n=2 ** 31 - 1),
+               dict(n=2 ** 31 - 1), dict(m=2 ** 31 - 1)):
         assert call(**kw) == vq.VQ_ERR_SHAPE, kw
     for kw in (dict(dt=BAD), dict(g=2), dict(g=-1)):
         assert call(**kw) == vq.VQ_ERR_UNSUPPORTED, kw
