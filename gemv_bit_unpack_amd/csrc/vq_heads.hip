@@ -356,6 +356,8 @@ vq_status launch_heads(const HeadsArgs& args, void* stream) {
   if (tt == 1 && all < kWorkgroups) per = groups;  // one head for each group
   const int64_t gx = (all + tt - 1) / tt, gy = ((int64_t)heads + per - 1) / per;
   if (gy > 65535 || !grid_ok(gx * gy, kThreads)) return VQ_ERR_SHAPE;
+  // one's output where the other is read or written: workgroups take the heads of both in any order
+  if (a.heads[0] > 0 && a.heads[1] > 0 && (a.y[0] == a.y[1] || a.y[0] == a.x[1] || a.y[1] == a.x[0])) return VQ_ERR_UNSUPPORTED;
   // Outputs that the L2s (8 of 4 MB) would not hold for whoever reads them next go past them: 8192 tokens of 64 + 8 heads of
   // 128 in bf16, 151 MB each way, 74 us through the caches and 62 past them (with norms 75 and 67, half a head rotated 97 and
   // 73); 512 tokens of 32 + 8 heads 6.7 us either way

@@ -569,7 +569,7 @@ typedef struct vq_heads_desc {
  * and v elsewhere, with t = 2 pi positions[batch][token] freqs[j].  freqs: device, double [rot / 2], turns per position;
  * positions: device, any sign (-p undoes p), exact up to 2^53: the angle is formed and reduced in fp64.  Weights and biases
  * [dim] may each be NULL (1, 0), and are not taken without a norm.  An output may be its input itself where type and
- * strides are the same; otherwise no output overlaps an input.  Pointers are element-aligned. */
+ * strides are the same; otherwise no output overlaps an input or the other output.  Pointers are element-aligned. */
 vq_status vq_rotate_heads(const vq_heads_desc* desc, const void* q, const void* k, const void* positions,
                           const double* freqs, const void* q_w, const void* q_b, const void* k_w, const void* k_b,
                           void* q_out, void* k_out, void* stream);

@@ -120,3 +120,12 @@ def test_binding_refuses_host_tensors(vq):
         vq.rotate_heads(x, None, torch.zeros(2, dtype=torch.int64), None)
     with pytest.raises(ValueError, match="norm must be"):
         vq.rotate_heads(x, None, None, None, norm="l2")
+
+
+def test_one_tensor_written_over_the_other_is_refused(vq):
+    """Queries and keys exchanged, or both written to one place: the heads of both are taken in any order."""
+    fn = vq.lib().vq_rotate_heads
+    k, out = 1 << 21, 1 << 22
+    same = dict(k_heads=4, k_strides=(768, 256, 64), k_out_strides=(768, 256, 64))
+    for yq, yk in ((k, P), (out, out), (k, out), (out, P)):
+        assert fn(ctypes.byref(_desc(vq, **same)), P, k, P, P, *(None,) * 4, yq, yk, None) == vq.VQ_ERR_UNSUPPORTED, (yq, yk)
