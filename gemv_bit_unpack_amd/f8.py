@@ -209,6 +209,8 @@ class F8MLP:
     def __init__(self, w_in, s_in, w_out, s_out):
         torch = _torch()
         d, i = w_out.shape
+        if tuple(w_in.shape) != (2 * i, d):  # the padded rows of another width could be as long
+            raise ValueError("w_in must be %s, got %s" % ([2 * i, d], tuple(w_in.shape)))
         self.features, self.inner = d, i
         self.w_in, self.s_in, self.w_out, self.s_out = f8_pad(w_in), s_in, f8_pad(w_out), s_out
         e4m3 = torch.float8_e4m3fn

@@ -157,3 +157,10 @@ def test_binding_refusals(vq):
             call()
     with pytest.raises(ValueError, match="even number of rows"):
         vq.f8.f8_linear.__globals__["_outputs"](torch.zeros((3, 8)), True)
+
+
+def test_layer_refuses_another_width(vq):
+    """Columns that the padding of rows hides: w_in for 100 columns beside w_out for 120."""
+    e4 = lambda *s: torch.zeros(s, dtype=torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match=r"w_in must be \[32, 120\]"):
+        vq.F8MLP(e4(32, 100), torch.zeros((2, 1)), e4(120, 16), torch.zeros((1, 1)))
