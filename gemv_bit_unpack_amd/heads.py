@@ -207,6 +207,8 @@ def rotate_heads(q, k, positions, rotary, *, norm="none", q_weight=None, q_bias=
         rot, start, inter, scale, freqs_p = rotary.dim, rotary.start, int(rotary.interleaved), rotary.scale, rotary._p
         if rotary._dev != dev:
             raise ValueError("rotary must be on device %d, is on %s" % (dev, rotary.freqs.device))
+        if positions is None:
+            raise TypeError("positions must be given with a rotary")
         if positions.dtype is torch.int64:
             wide = 1
         elif positions.dtype is not torch.int32:

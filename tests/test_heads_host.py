@@ -129,3 +129,9 @@ def test_one_tensor_written_over_the_other_is_refused(vq):
     same = dict(k_heads=4, k_strides=(768, 256, 64), k_out_strides=(768, 256, 64))
     for yq, yk in ((k, P), (out, out), (k, out), (out, P)):
         assert fn(ctypes.byref(_desc(vq, **same)), P, k, P, P, *(None,) * 4, yq, yk, None) == vq.VQ_ERR_UNSUPPORTED, (yq, yk)
+
+
+def test_rotation_needs_positions(vq, monkeypatch):
+    monkeypatch.setattr(vq.heads, "_device", lambda t, what: -1)
+    with pytest.raises(TypeError, match="positions"):
+        vq.rotate_heads(torch.zeros((2, 4, 8)), None, None, vq.Rotary(8, device="cpu"))
