@@ -517,21 +517,20 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void f8_tile_kernel(F8Args a, in
   tile<BM, BN, WM, WN, NB, KG, WIDE, GATED, SPLIT, false>(a, mt * BM, nti * (GATED ? BN / 2 : BN), lds, sbs, nullptr);
 }
 
-// 8 wavefronts, one workgroup per CU: 256 x 256 tiles, or 128 x 256 ones where the operands go to fp16 (their fragments
-// take twice the registers).  256 x 256: 128 rows only where the matrix's last tile has no more left, and in the last round
+// 8 wavefronts, one workgroup per CU: 256 x 256 tiles, or 128 x 256 ones for outputs in 8 bits, whose operands go to fp16
+// (their fragments take twice the registers).  256 x 256: 128 rows only where the matrix's last tile has no more left, and in the last round
 // over the 256 CUs if at most half of them have a tile in it: two half tiles for each then take half a round.
-template <bool WIDE, bool GATED, bool OUTQ>
+template <bool GATED, bool OUTQ>
 __global__ __launch_bounds__(512) void f8_big_kernel(F8Args a, int32_t nt, int32_t mt_count) {
-  constexpr int kSteps = WIDE ? 3 * step_bytes(128, 256) : 2 * step_bytes(256, 256);
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSteps + 4096 + (OUTQ ? 16 * (WIDE ? 128 : 256) : 0)];
+  constexpr int kSteps = OUTQ ? 3 * step_bytes(128, 256) : 2 * step_bytes(256, 256);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSteps + 4096 + (OUTQ ? 16 * 128 : 0)];
   float* const sbs = (float*)(lds + kSteps);
-  float* const tops = sbs + 1024;
   const int32_t total = mt_count * nt;
   const int32_t id = (int32_t)blockIdx.x;
   int32_t mt, nti, part = 0;
-  if constexpr (WIDE) {
+  if constexpr (OUTQ) {
     if (!place(id, total, mt_count, nt, mt, nti)) return;
-    tile<128, 256, 2, 4, 3, 1, true, GATED, false, OUTQ>(a, mt * 128, nti * (GATED ? 128 : 256), lds, sbs, tops);
+    tile<128, 256, 2, 4, 3, 1, true, GATED, false, true>(a, mt * 128, nti * 128, lds, sbs, sbs + 1024);
   } else {
     const int32_t rest = total % 256;
     const int32_t full = rest <= 128 ? total - rest : total;  // ids from the next multiple of 8 on are halves
@@ -548,9 +547,9 @@ __global__ __launch_bounds__(512) void f8_big_kernel(F8Args a, int32_t nt, int32
     const int32_t row0 = mt * 256 + part * 128, n0 = nti * (GATED ? 128 : 256);
     if (row0 >= a.m) return;
     if (half || a.m - row0 <= 128) {
-      tile<128, 256, 2, 4, 2, 1, false, GATED, false, OUTQ>(a, row0, n0, lds, sbs, tops);
+      tile<128, 256, 2, 4, 2, 1, false, GATED, false, false>(a, row0, n0, lds, sbs, nullptr);
     } else {
-      tile<256, 256, 2, 4, 2, 1, false, GATED, false, OUTQ>(a, row0, n0, lds, sbs, tops);
+      tile<256, 256, 2, 4, 2, 1, false, GATED, false, false>(a, row0, n0, lds, sbs, nullptr);
     }
   }
 }
@@ -878,15 +877,15 @@ vq_status launch_tile(const F8Args& a, hipStream_t st, bool check_only) {
       <<<dim3(blocks, SPLIT ? a.plan.splits : 1), dim3(kThreads), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
   return done();
 }
-template <bool WIDE, bool GATED, bool OUTQ>
+template <bool GATED, bool OUTQ>
 vq_status launch_big(const F8Args& a, hipStream_t st, bool check_only) {
-  constexpr int rows = WIDE ? 128 : 256, out = GATED ? 128 : 256;
+  constexpr int rows = OUTQ ? 128 : 256, out = GATED ? 128 : 256;
   const int64_t mt = ((int64_t)a.m + rows - 1) / rows;
   const int64_t nt = ((int64_t)a.n + out - 1) / out;
-  const int64_t blocks = WIDE ? (mt * nt + 7) / 8 * 8 : mt * nt + 128 + 8;  // at most 128 tiles are cut in two
+  const int64_t blocks = OUTQ ? (mt * nt + 7) / 8 * 8 : mt * nt + 128 + 8;  // at most 128 tiles are cut in two
   if (!vqi::grid_ok(blocks, 512)) return VQ_ERR_SHAPE;
   if (check_only) return VQ_OK;
-  f8_big_kernel<WIDE, GATED, OUTQ><<<dim3((uint32_t)blocks), dim3(512), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
+  f8_big_kernel<GATED, OUTQ><<<dim3((uint32_t)blocks), dim3(512), 0, st>>>(a, (int32_t)nt, (int32_t)mt);
   return done();
 }
 
@@ -1015,11 +1014,11 @@ vq_status run(const F8Args& a, hipStream_t st, bool check_only) {
     case k128x128: return tiles<128, 128, 4, 2, 3, 1, WIDE>(a, st, check_only);
     case k128x128Pair: return tiles<128, 128, 2, 2, 2, 1, WIDE>(a, st, check_only);
     default:
-      if (!a.y) return launch_big<WIDE, true, true>(a, st, check_only);
-      if constexpr (!WIDE) {
-        return a.gated ? launch_big<false, true, false>(a, st, check_only) : launch_big<false, false, false>(a, st, check_only);
+      if constexpr (WIDE) {
+        return a.y ? VQ_ERR_UNSUPPORTED : launch_big<true, true>(a, st, check_only);  // no plan has the first
+      } else {
+        return a.gated ? launch_big<true, false>(a, st, check_only) : launch_big<false, false>(a, st, check_only);
       }
-      return VQ_ERR_UNSUPPORTED;  // no plan has it
   }
 }
 
@@ -1092,11 +1091,11 @@ F8Plan f8_plan(int32_t m, int32_t n, int32_t k, bool gated, bool wide, bool may_
   return best;
 }
 
-bool f8_big_plan(int32_t m, int32_t n, int32_t k, bool wide, F8Plan& plan) {
+bool f8_big_plan(int32_t m, int32_t n, int32_t k, F8Plan& plan) {
   // what the hidden rows cost otherwise: written and read in fp32, written in 8 bits, in a launch of their own
   const float spared = kQuantStart + 9.f * (float)m * (float)n / kQuantRate;
-  const Shape s(m, n, k, true, wide);
-  if (cost(s, k256x256, 1, false, wide) > cost(s, plan.way, plan.splits, plan.cut, wide) + spared) return false;
+  const Shape s(m, n, k, true, true);
+  if (cost(s, k256x256, 1, false, true) > cost(s, plan.way, plan.splits, plan.cut, true) + spared) return false;
   plan = F8Plan{k256x256, 1, false};
   return true;
 }

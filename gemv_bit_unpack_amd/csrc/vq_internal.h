@@ -276,7 +276,7 @@ struct F8Args {
   const float* sw;       // [f8_blocks(n), twice with the gate][f8_blocks(k)]
   const uint16_t* bias;  // fp16 [n or 2 n] or nullptr
   int32_t gated;         // y = silu(g) u, g and u the two halves of w's rows
-  int32_t wide;          // the products' operands go to fp16, for sums that are exact to fp32 (fp32 outputs)
+  int32_t wide;          // the products' operands go to fp16, for sums that are exact to fp32 (fp32 and 8-bit outputs)
   void* y;               // [m][n], or nullptr: yq and ys take the outputs in 8 bits
   vq_dtype y_dtype;
   uint8_t* yq;  // [m][q8_row_bytes(n)]
@@ -286,8 +286,8 @@ struct F8Args {
 // The plan of a product of m >= 1 rows and n >= 1 outputs; may_cut: the tokens come as they are, and a plan that does not cut
 // them inside pays for the launch that does.
 F8Plan f8_plan(int32_t m, int32_t n, int32_t k, bool gated, bool wide, bool may_cut);
-// A gated product whose outputs are to be cut to 8 bits, by `plan` as it is or, true, by one that writes them so (yq, ys).
-bool f8_big_plan(int32_t m, int32_t n, int32_t k, bool wide, F8Plan& plan);
+// A gated product (wide) whose outputs are to be cut to 8 bits, by `plan` as it is or, true, by one that writes them so (yq, ys).
+bool f8_big_plan(int32_t m, int32_t n, int32_t k, F8Plan& plan);
 vq_status launch_f8(const F8Args& a, void* stream, bool check_only = false);
 
 // Norms and rotation of heads (validated arguments; vq_heads.hip).
