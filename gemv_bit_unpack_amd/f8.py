@@ -222,6 +222,8 @@ class F8MLP:
         """From dense weights gate and up [I, D] and out [D, I], cut to 8 bits in blocks."""
         torch = _torch()
         d, i = out.shape
+        if tuple(gate.shape) != (i, d) or tuple(up.shape) != (i, d):  # behind the padding of rows it would not be seen
+            raise ValueError("gate and up must be %s, got %s and %s" % ([i, d], tuple(gate.shape), tuple(up.shape)))
         (g, gs), (u, us), (o, os) = (f8_quantize(w, BLOCK) for w in (gate, up, out))
         w_in = torch.cat((g.view(torch.uint8), u.view(torch.uint8))).view(torch.float8_e4m3fn)
         return cls(w_in[:, :d], torch.cat((gs, us)), o[:, :i], os)

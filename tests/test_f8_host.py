@@ -164,3 +164,21 @@ def test_layer_refuses_another_width(vq):
     e4 = lambda *s: torch.zeros(s, dtype=torch.float8_e4m3fn)
     with pytest.raises(ValueError, match=r"w_in must be \[32, 120\]"):
         vq.F8MLP(e4(32, 100), torch.zeros((2, 1)), e4(120, 16), torch.zeros((1, 1)))
+
+
+@pytest.mark.parametrize("gate,up,out", [((16, 100), (16, 100), (120, 16)),   # columns that the padding of rows hides
+                                         ((16, 128), (16, 128), (100, 16)),   # columns that would be cut off
+                                         ((17, 100), (15, 100), (100, 16)),   # rows that add up to both halves
+                                         ((16, 100), (16, 99), (100, 16)), ((32, 100), (0, 100), (100, 16)),
+                                         ((16, 100), (16, 100), (100, 17))])
+def test_from_weights_refuses_other_shapes(vq, monkeypatch, gate, up, out):
+    cut = []
+    monkeypatch.setattr(vq.f8, "f8_quantize", lambda w, *a: cut.append(w) or (
+        torch.zeros((w.shape[0], vq.q8_row_bytes(w.shape[1])), dtype=torch.float8_e4m3fn),
+        torch.zeros((vq.f8_blocks(w.shape[0]), vq.f8_blocks(w.shape[1])))))
+    monkeypatch.setattr(vq.q8, "_device", lambda t, what: -1)
+    with pytest.raises(ValueError, match="gate and up must be"):
+        vq.F8MLP.from_weights(*(torch.zeros(s) for s in (gate, up, out)))
+    assert not cut
+    layer = vq.F8MLP.from_weights(*(torch.zeros(s) for s in ((16, 100), (16, 100), (100, 16))))
+    assert (layer.features, layer.inner) == (100, 16) and len(cut) == 3
