@@ -452,6 +452,9 @@ class Q8Experts:
     def __init__(self, w_in, s_in, w_out, s_out):
         torch = _torch()
         e, d, i = w_out.shape
+        # the padded rows of another width could be as long; rows that are padded already are taken as before
+        if tuple(w_in.shape) not in ((e, 2 * i, d), (e, 2 * i, q8_row_bytes(d))):
+            raise ValueError("w_in must be %s, got %s" % ([e, 2 * i, d], tuple(w_in.shape)))
         self.experts, self.features, self.inner = e, d, i
         self.w_in, self.s_in, self.w_out, self.s_out = q8_pad(w_in), s_in, q8_pad(w_out), s_out
         self._p = _Weights(w_in=(self.w_in, (e, 2 * i, q8_row_bytes(d)), torch.int8),
