@@ -125,7 +125,8 @@ __global__ __launch_bounds__(256) void f8_tokens_kernel(F8QuantArgs a) {
 template <vq_dtype XT>
 __global__ __launch_bounds__(256) void f8_weights_kernel(F8QuantArgs a) {
   __shared__ uint32_t part[4];
-  const int32_t kb = (int32_t)blockIdx.x, nb = (int32_t)blockIdx.y;
+  const int32_t blocks = (int32_t)vqi::f8_blocks(a.k);
+  const int32_t nb = (int32_t)blockIdx.x / blocks, kb = (int32_t)blockIdx.x - nb * blocks;
   const int col = (threadIdx.x & 15) * 8, row0 = nb * 128 + (threadIdx.x >> 4);
   constexpr int es = XT == VQ_F32 ? 4 : 2;
   const int32_t end = min(a.rows, nb * 128 + 128);
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(256) void f8_weights_kernel(F8QuantArgs a) {
       *(uint2*)(a.q + (int64_t)r * ld + kb * kStep + col) =
           make_uint2(vqd::f8_pack4(f[j], sc), vqd::f8_pack4(f[j] + 4, sc));
   }
-  if (threadIdx.x == 0) a.s[(int64_t)nb * gridDim.x + kb] = sc.s;
+  if (threadIdx.x == 0) a.s[blockIdx.x] = sc.s;
 }
 
 // ---------------------------------------------------------------- tiles
@@ -1042,9 +1043,9 @@ vq_status launch_f8_tokens(const F8QuantArgs& a, void* stream, bool check_only) 
 
 vq_status launch_f8_weights(const F8QuantArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  const int64_t kb = f8_blocks(a.k), nb = f8_blocks(a.rows);
-  if (nb > 65535) return VQ_ERR_SHAPE;
-  const dim3 g((uint32_t)kb, (uint32_t)nb), b(256);
+  const int64_t blocks = f8_blocks(a.k) * f8_blocks(a.rows);
+  if (!grid_ok(blocks, 256)) return VQ_ERR_SHAPE;
+  const dim3 g((uint32_t)blocks), b(256);
   switch (a.x_dtype) {
     case VQ_F32: f8_weights_kernel<VQ_F32><<<g, b, 0, st>>>(a); break;
     case VQ_F16: f8_weights_kernel<VQ_F16><<<g, b, 0, st>>>(a); break;
