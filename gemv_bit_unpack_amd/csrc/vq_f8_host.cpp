@@ -223,6 +223,7 @@ vq_status vq_f8_linear(int32_t M, int32_t N, int32_t K, const void* x, vq_dtype 
       !aligned(y, size_of(y_dtype)) || misaligned(workspace, 256))
     return VQ_ERR_ALIGN;
   if (workspace_bytes < ws.bytes) return VQ_ERR_BUFFER_SIZE;
+  if (x == y) return VQ_ERR_UNSUPPORTED;  // tokens that are cut inside are read while outputs are stored
   const F8Args a = product(M, N, K, w, sw, bias, gated, y, y_dtype);
   if ((st = linear(a, x, x_dtype, ldx, ws, stream, true)) != VQ_OK) return st;
   return linear(a, x, x_dtype, ldx, ws, stream, false);

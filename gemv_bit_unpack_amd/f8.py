@@ -126,7 +126,7 @@ def f8_gemm(q, s, w, sw, bias, k, gated=False, ws=None, y_dtype=None, out=None):
 
 def f8_linear(x, w, sw, bias, ws, gated=False, y_dtype=None, out=None):
     """f8_gemm on x [M, K] cut to 8 bits inside the call; ``ws``: a uint8 device buffer of f8_linear_workspace_bytes (None
-    where that is 0)."""
+    where that is 0); ``out`` does not overlap x."""
     p, ld, code, dev = _rows(x, "x")
     (m, k), n = x.shape, _outputs(w, gated)
     out = _out(out, (m, n), y_dtype or x.dtype, x)

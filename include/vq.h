@@ -504,6 +504,7 @@ vq_status vq_block_norm(const vq_norm_desc* desc, const void* z, const void* h, 
  * equal bits.  Within a block the products are summed in fp32 too for y_dtype fp32.  For 16-bit outputs the shape decides: in
  * fp32 again where up to 16 rows are streamed, else by the 8-bit matrix instruction, which cuts each product below 2^-13 of
  * the largest of its eight: a block's sum is off by 1.4e-5 of its spread (measured; half a step of fp16 is 2.4e-4).
+ * An output overlaps no input and no workspace (vq_f8_mlp's y may be x).
  * vq_f8_mlp forms its hidden rows as for fp32 outputs, whatever y_dtype: which e4m3 value they take rests on their sums.
  */
 

@@ -182,3 +182,10 @@ def test_from_weights_refuses_other_shapes(vq, monkeypatch, gate, up, out):
     assert not cut
     layer = vq.F8MLP.from_weights(*(torch.zeros(s) for s in ((16, 100), (16, 100), (100, 16))))
     assert (layer.features, layer.inner) == (100, 16) and len(cut) == 3
+
+
+def test_outputs_over_the_input_are_refused(vq):
+    """Tokens that are cut inside the product are read by every workgroup, while others store: y may not be x."""
+    f, out = vq.lib().vq_f8_linear, 1 << 21
+    for m in (1, 8, 64):  # the tokens cut inside, and by a launch in front
+        assert f(m, 64, 64, P, F16, 64, out, out, None, 0, P, F16, out, 1 << 40, None) == vq.VQ_ERR_UNSUPPORTED
