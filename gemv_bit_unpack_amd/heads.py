@@ -143,11 +143,15 @@ def _plan(q, k, positions, q_out, k_out, wide, rot, start, inter, kind, x_dtype,
     if start + rot > d:
         raise ValueError("the rotated part ends at %d, a head at %d" % (start + rot, d))
     pos_stride = 0
-    if positions is not None and tuple(positions) != (t,):
-        if len(q[0]) != 4 or tuple(positions) != (b, t):
+    if positions is not None:
+        shape, strides = positions
+        if tuple(shape) != (t,) and (len(q[0]) != 4 or tuple(shape) != (b, t)):
             raise ValueError("positions must be [%d]%s, got %s" % (t, " or [%d, %d]" % (b, t) if len(q[0]) == 4 else "",
-                                                                  tuple(positions)))
-        pos_stride = t
+                                                                  tuple(shape)))
+        if t > 1 and strides[-1] != 1:
+            raise ValueError("positions of neighbouring tokens must be neighbours")
+        if len(shape) == 2 and b > 1:
+            pos_stride = strides[0]
     triple = ctypes.c_int64 * 3
     return ctypes.byref(HeadsDesc(b, t, hq, hk, d, rot, start, inter, kind, _code(x_dtype), _code(y_dtype),
                                   VQ_F32 if w_dtype is None else _code(w_dtype), wide, pos_stride, triple(*qs), triple(*ks),
@@ -171,10 +175,10 @@ def rotate_heads(q, k, positions, rotary, *, norm="none", q_weight=None, q_bias=
 
     q [tokens, q heads, dim] or [batch, tokens, q heads, dim], k the same with its own number of heads, or None; any strides
     but of dim (views of one projection's output; [batch, heads, tokens, dim] transposed).  positions int32 or int64
-    [tokens] or [batch, tokens] (one row for all batches with [tokens]); ``rotary``: a Rotary, or None for norms alone
-    (positions are then not read).  norm: "none", "rms" or "layer" over each head, weights and biases [dim].  ``q_out``,
-    ``k_out``: tensors to write into, of any strides, q and k themselves too; by default new contiguous ones of
-    ``out_dtype`` (q's)."""
+    [tokens] or [batch, tokens] (one row for all batches with [tokens]; rows of any stride, expanded ones too); ``rotary``: a
+    Rotary, or None for norms alone (positions are then not read).  norm: "none", "rms" or "layer" over each head, weights
+    and biases [dim].  ``q_out``, ``k_out``: tensors to write into, of any strides, q and k themselves too; by default new
+    contiguous ones of ``out_dtype`` (q's)."""
     torch = _torch()
     kind = _KINDS.get(norm)
     if kind is None:
@@ -213,7 +217,9 @@ def rotate_heads(q, k, positions, rotary, *, norm="none", q_weight=None, q_bias=
             wide = 1
         elif positions.dtype is not torch.int32:
             raise TypeError("positions has dtype %s, expected int32 or int64" % positions.dtype)
-        pos, pos_p = positions.shape, _ptr(positions, "positions", None, dev)
+        if positions.get_device() != dev:
+            raise ValueError("positions must be on device %d, is on %s" % (dev, positions.device))
+        pos, pos_p = (positions.shape, positions.stride()), positions.data_ptr()
     desc = _plan((q.shape, q.stride()), k_view, pos, q_strides, k_strides, wide, rot, start, inter, kind, x_dtype, y_dtype,
                  w_dtype, float(scale) + 0.0, float(eps) + 0.0, float(weight_offset) + 0.0)  # + 0.0: -0.0 is found as 0.0
     _launch(lib().vq_rotate_heads, dev, desc, q.data_ptr(), kp, pos_p, freqs_p, *vecs, q_out.data_ptr(), kyp, _stream(dev))

@@ -135,3 +135,29 @@ def test_rotation_needs_positions(vq, monkeypatch):
     monkeypatch.setattr(vq.heads, "_device", lambda t, what: -1)
     with pytest.raises(TypeError, match="positions"):
         vq.rotate_heads(torch.zeros((2, 4, 8)), None, None, vq.Rotary(8, device="cpu"))
+
+
+def test_positions_of_any_batch_stride(vq, monkeypatch):
+    """[batch, tokens] as views: expanded from one row, every other row, a column of a wider tensor; not every other token."""
+    seen = []
+    monkeypatch.setattr(vq.heads, "_device", lambda t, what: -1)
+    monkeypatch.setattr(vq.heads, "_stream", lambda dev: 0)
+    monkeypatch.setattr(vq.heads, "_launch", lambda fn, dev, desc, *a: seen.append((desc._obj, a[2])))
+    rotary = vq.Rotary(8, device="cpu")
+    q = torch.zeros((3, 5, 2, 8))
+    wide = torch.arange(6 * 9).view(6, 9)
+    for pos, stride in ((wide[0, :5], 0), (wide[0, :5].expand(3, 5), 0), (wide[::2, 2:7], 18), (wide[:3, :5].contiguous(), 5),
+                        (wide[:3, :5].int(), 5)):
+        vq.rotate_heads(q, None, pos, rotary)
+        desc, p = seen.pop()
+        assert (desc.position_stride, desc.positions_64, p) == (stride, int(pos.dtype is torch.int64), pos.data_ptr())
+    for one, stride in ((wide[:3, 4:5], 9), (wide[4:5, :3].t(), 1)):  # a decode step: one position for each batch
+        vq.rotate_heads(q[:, :1], None, one, rotary)
+        assert seen.pop()[0].position_stride == stride
+    vq.rotate_heads(q[:1], None, wide[2:3, :5], rotary)
+    vq.rotate_heads(q[0, :1], None, wide[0, :1], rotary)
+    seen.clear()
+    for pos in (wide[:3, :9:2], wide[0, :9:2], wide[:5, :3].t(), wide[0, :1].expand(5), wide[:1, :5]):
+        with pytest.raises(ValueError, match="positions"):
+            vq.rotate_heads(q, None, pos, rotary)
+    assert not seen
