@@ -6,8 +6,12 @@
 // added to the output's fp32 sum with the product of its two scales: one fused multiply-add per output and block, beside
 // 128 multiply-adds of the matrix pipe.  That is half of the vector pipe's time under the matrix pipe's whole.
 //
-// Up to some hundred rows the weights' bytes bound it (one row of 28672 x 8192: 42 us, 5.6 TB/s), above that the matrix pipe
-// at the clock that the card holds (8192^3: 479 us, 2.3 PFLOP/s; a library product with one scale for all 414 us).
+// Weights that fill the memory's time bound it up to some hundred rows (one row of 28672 x 8192: 42 us, 5.6 TB/s; 128 of
+// 8192 x 28672: 54 us, 4.3).  Smaller ones, from 17 rows on, take 2 to 4 times as long as their bytes: a CU has one tile or
+// two, a step of which is a chain of loads, barrier, fragments and products (37 x 5003 x 4099: 14 us, the matrix pipe busy a
+// tenth of it).  Prompts fill no pipe: 8192^3 takes 479 to 514 us (2.1 to 2.3 PFLOP/s; a library product with one scale for
+// all 414 to 427), with the matrix pipe busy 52 % of the cycles, at 2.0 GHz, the vector pipe 41 % and wavefronts waiting for
+// 29 % of theirs.
 //
 // Rows of q and w are whole 128-byte steps with zero pads, so no kernel has a K edge; rows past an edge of a tile read the
 // last valid row again and are not stored.  A sum's order is fixed by the shape (waves, then K splits, in order): equal
@@ -519,7 +523,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void f8_tile_kernel(F8Args a, in
 }
 
 // 8 wavefronts, one workgroup per CU: 256 x 256 tiles, or 128 x 256 ones for outputs in 8 bits, whose operands go to fp16
-// (their fragments take twice the registers).  256 x 256: 128 rows only where the matrix's last tile has no more left, and in the last round
+// (their fragments take twice the registers; their conversions take as much of the vector pipe, 57 % of the cycles, as the
+// products of the matrix pipe, 45 %: 2048 tokens, 14336 pairs of 4096 columns 494 to 507 us).  256 x 256: 128 rows only where the matrix's last tile has no more left, and in the last round
 // over the 256 CUs if at most half of them have a tile in it: two half tiles for each then take half a round.
 template <bool GATED, bool OUTQ>
 __global__ __launch_bounds__(512) void f8_big_kernel(F8Args a, int32_t nt, int32_t mt_count) {
@@ -960,8 +965,9 @@ float cost(const Shape& s, int32_t way, int32_t splits, bool cut, bool wide) {
   if (way <= kStream2) {
     // two workgroups on each CU, that take turns with the memory: parts of a round count as such
     const float rounds = (float)columns * (float)splits * (1.f / kFewWorkgroups);
-    // cut inside, single blocks with eight steps of a wavefront or more, whole sets, keep their loads going: 1 x 28672 x 8192
-    // 43 us, 48 in groups of two; 2 x 28672 x 5120 (five steps) 36 and 34
+    // cut inside, single blocks with eight steps of a wavefront or more keep their loads going, most of all whole sets of four:
+    // of 28672 outputs with eight steps (K = 8192) 42 us and 48 in groups of two, with nine and ten 51 to 54 either way, with
+    // twelve 72 and 77, with sixteen 92 and 101; with five 34 and 33
     const float going = cut && way == kStream1 && steps >= 8.f ? 0.8f : 1.f;
     t += steps * (rounds <= 0.5f ? c.step[0] : going * c.step[1] * std::max(rounds, 1.f));
     if (cut) t += kCutStart[way] + kCutPiece * 0.125f * (float)s.m * steps;

@@ -3,9 +3,10 @@
 //   v = N(x) over a head's values (identity, RMS or centred, weight and bias)
 //   pairs (a, b) of the rotated part:  a' = c (a cos t - b sin t),  b' = c (a sin t + b cos t),  t = position * frequency
 //
-// The angle is formed in fp64, in turns, and reduced there to an eighth of a turn: what is left goes to fp32 with an error
-// of 2^-27 turns at any position.  The sines of a workgroup's tokens are computed once, one pair per thread, and shared by
-// all heads in LDS.
+// The angle is formed in fp64, in turns, where the product is off by 2^-53 of itself at most, and reduced there to an eighth
+// of a turn: what is left goes to fp32 with an error of 2^-27 turns.  That is the larger one up to 2^26 turns (2^28 positions
+// of a pair that turns by one radian each); at 2^40 positions the product's is 2^-16 turns, at 2^52 2^-4.  The sines of a
+// workgroup's tokens are computed once, one pair per thread, and shared by all heads in LDS.
 //
 // A head is held by L lanes (a power of two), 16 values each: 8 pairs of the rotated part, or 16 values of the parts beside
 // it.  Every value is read once and written once; the norm's sums go over the L lanes, up to 16 of them without LDS.

@@ -568,9 +568,10 @@ typedef struct vq_heads_desc {
  *   v = N(x)                                       over the head's dim values, N as in vq_block_norm
  *   a' = scale (a cos t - b sin t),  b' = scale (a sin t + b cos t)   for the pairs (a, b) of the rotated part
  * and v elsewhere, with t = 2 pi positions[batch][token] freqs[j].  freqs: device, double [rot / 2], turns per position;
- * positions: device, any sign (-p undoes p), exact up to 2^53: the angle is formed and reduced in fp64.  Weights and biases
- * [dim] may each be NULL (1, 0), and are not taken without a norm.  An output may be its input itself where type and
- * strides are the same; otherwise no output overlaps an input or the other output.  Pointers are element-aligned. */
+ * positions: device, any sign (-p undoes p), converted exactly up to 2^53: the angle is formed in fp64, off by 2^-53 of its
+ * turns at most, and reduced there.  Weights and biases [dim] may each be NULL (1, 0), and are not taken without a norm.  An
+ * output may be its input itself where type and strides are the same; otherwise no output overlaps an input or the other
+ * output.  Pointers are element-aligned. */
 vq_status vq_rotate_heads(const vq_heads_desc* desc, const void* q, const void* k, const void* positions,
                           const double* freqs, const void* q_w, const void* q_b, const void* k_w, const void* k_b,
                           void* q_out, void* k_out, void* stream);
